@@ -437,6 +437,159 @@ int ds4a_hca_attend_fp8(const ds4a_layer_cfg* cfg, int B, int T_q, const int32_t
                         int64_t win_bstride, const float* sink, ds4a_bf16* out, void* ws,
                         size_t ws_bytes, ds4a_stream stream);
 
+/*
+ * Paged K=V cache.  The rows of a layer's compressed entries lie in pages of
+ * page_size rows anywhere in one allocation; a table lists the physical page
+ * of every logical page of a sequence.  (No counterpart on the pages of the
+ * sources: contiguous pools must be reserved for the longest context.)
+ *
+ * Sequence b at position p has closed floor((p + 1) / m) entries; drop[b] of
+ * them have been evicted (ds4a_paged_evict; drop NULL: none).  The others
+ *   n = clamp(floor((p + 1) / m) - drop[b], 0, max_pages * page_size)
+ * lie in its slots 0 .. n - 1; slot s is row s % page_size of the physical
+ * page table[b][s / page_size].
+ *
+ *   pages        device, 16-byte aligned: n_pages * page_size rows, of 2 D
+ *                bytes (format 0, bf16) or ds4a_kv_fp8_row_bytes(D, R) bytes
+ *                (DS4A_MX_KV_FP8)
+ *   page_size    rows of a page, any number >= 1
+ *   table        device int32, max_pages entries a sequence, table_stride
+ *                apart.  Only the pages of slots in use are read; an entry
+ *                outside [0, n_pages) there is recorded as
+ *                DS4A_DEV_BAD_INDEX and its rows take no part
+ * At most 2^30 slots a sequence and 2^31 - 1 rows in all.
+ */
+typedef struct ds4a_paged_kv {
+  void* pages;
+  const int32_t* table;
+  int64_t table_stride;
+  int32_t format; /* 0 or DS4A_MX_KV_FP8 */
+  int32_t n_pages, page_size, max_pages;
+} ds4a_paged_kv;
+
+/* Bytes of workspace ds4a_paged_attend needs (0: bad arguments). */
+size_t ds4a_paged_attend_workspace(const ds4a_layer_cfg* cfg, const ds4a_paged_kv* kv, int B, int sparse,
+                                   int weights);
+
+/*
+ * ds4a_paged_attend -- ds4a_sparse_attend / ds4a_hca_attend of one new token
+ * per sequence over a paged cache: the same keys, softmax with sink, and
+ * rotations, the keys split over the GPU and joined.
+ *
+ *   q_pos   device int32 [B].  A negative position is recorded as
+ *           DS4A_DEV_BAD_POS and its output and weights are left as they were
+ *   q       device bf16 [B, H, D]; q_norm_g, win, sink, out as the
+ *           contiguous calls (win may be NULL when cfg->window is 0)
+ *   drop    device int32 [B] or NULL
+ *   idx     device int32 [B, k] or NULL (every slot in use).  Slots to
+ *           attend to, -1 for none; of a row only the first min(k, n) places
+ *           are read, which hold every valid slot of a row that is packed to
+ *           the left without repeats, as ds4a_index_topk writes it.  A slot
+ *           outside [0, n) is recorded as DS4A_DEV_BAD_INDEX and skipped
+ *   weights device bf16 [B, w_len], rows w_stride apart, or NULL: for every
+ *           slot in use the probability that this token gave it, summed over
+ *           the heads (the sink and the window keep the rest).  Slots not in
+ *           use are left as they were.  Not with idx (DS4A_EUNSUPPORTED).  If
+ *           a sequence has more than w_len slots in use, those behind are not
+ *           written and DS4A_DEV_BAD_INDEX is recorded
+ *   ws      device workspace of ds4a_paged_attend_workspace(...) bytes; two
+ *           calls that may run at the same time need one each
+ * The launch does not depend on the positions, so that a captured graph
+ * serves later steps as the sequences grow.
+ */
+int ds4a_paged_attend(const ds4a_layer_cfg* cfg, const ds4a_paged_kv* kv, int B, const int32_t* q_pos,
+                      const ds4a_bf16* q, const float* q_norm_g, const int32_t* drop, const int32_t* idx,
+                      const ds4a_bf16* win, int win_cap, int64_t win_bstride, const float* sink, ds4a_bf16* out,
+                      ds4a_bf16* weights, int w_len, int64_t w_stride, void* ws, size_t ws_bytes,
+                      ds4a_stream stream);
+
+/*
+ * ds4a_paged_append -- ds4a_compress_append(_mx) into a paged cache: the
+ * entry i that a token closes goes to slot i - drop[b].  c = cfg->head_dim
+ * channels; kv->format 0 or DS4A_MX_KV_FP8.  A slot at or behind max_pages *
+ * page_size, a negative slot or a bad page is recorded as
+ * DS4A_DEV_BAD_INDEX and the entry is not stored (its rows still enter the
+ * state).
+ */
+int ds4a_paged_append(const ds4a_layer_cfg* cfg, const ds4a_paged_kv* kv, int B, const int32_t* pos,
+                      const int32_t* drop, const ds4a_bf16* ca, const ds4a_bf16* cb, const ds4a_bf16* za,
+                      const ds4a_bf16* zb, const float* bias_a, const float* bias_b, const float* norm_g,
+                      ds4a_bf16* state, ds4a_stream stream);
+
+/* Bytes of workspace ds4a_paged_evict needs (0: bad arguments). */
+size_t ds4a_paged_evict_workspace(const ds4a_paged_kv* kv, int B);
+
+/*
+ * ds4a_paged_evict -- bound a paged cache to `budget` entries a sequence, by
+ * accumulated attention weight (for layers that attend to every entry; no
+ * counterpart on the pages of the sources).  For each sequence, with its n
+ * slots in use (as above; at most n_slots of them):
+ *   1. acc[s] += weights[s] for s < n (weights NULL: nothing is added);
+ *   2. if n > budget: of its n entries the `recent` youngest stay, and of the
+ *      others those of the largest acc (ties: the lower slot; NaN counts as
+ *      the largest), budget in all;
+ *   3. the kept entries in slots >= budget move, in order, into the slots
+ *      below budget that were left, with their rows, acc and entry number;
+ *      then acc = 0 and entry = -1 for all slots >= budget, entry of the
+ *      kept ones is their number, and drop[b] += n - budget.
+ * The order of the slots carries no meaning (an entry's row holds its
+ * position), so no other row moves.
+ *
+ *   q_pos   device int32 [B], the position of the last token appended
+ *           (negative: recorded as DS4A_DEV_BAD_POS, nothing is done)
+ *   acc     device float [B, n_slots], entry device int32 [B, n_slots], rows
+ *           `stride` apart; a sequence starts with acc 0, entry -1, drop 0.
+ *           entry -1 stands for the number s + drop[b]
+ *   weights device bf16 [B, n_slots], rows w_stride apart, or NULL
+ *   budget  1 .. n_slots; recent 0 .. budget
+ *   ws      device workspace of ds4a_paged_evict_workspace(...) bytes
+ * Sequences must not share pages.  The pages behind the budget may be handed
+ * out again once the call is done.
+ */
+int ds4a_paged_evict(const ds4a_layer_cfg* cfg, const ds4a_paged_kv* kv, int B, const int32_t* q_pos,
+                     const ds4a_bf16* weights, int64_t w_stride, int budget, int recent, int n_slots, float* acc,
+                     int32_t* entry, int64_t stride, int32_t* drop, void* ws, size_t ws_bytes,
+                     ds4a_stream stream);
+
+/*
+ * Microscaled 4-bit matrices for products: E2M1 elements, one E8M0 scale per
+ * 32 consecutive values of a row, rounded as DS4A_MX_IDX_FP4.
+ *   codes   [rows][K / 2] bytes, element 2i in the low nibble
+ *   scales  blocks of 128 rows x 128 values of K, 512 bytes each: row r and
+ *           scale j of a block at byte (r % 32) * 16 + (r / 32) * 4 + j; the
+ *           K / 128 blocks of a row range lie side by side, row ranges follow
+ *           one another; the last is padded to 128 rows
+ * (the order in which the tensor core takes them).  K a multiple of 128.
+ */
+/* Bytes of the scales of a rows x K matrix (0: bad arguments). */
+size_t ds4a_mxfp4_scale_bytes(int rows, int K);
+
+/* bf16 rows in[n_rows][in_stride] -> codes and scales (padding rows get scale
+ * 0).  Device pointers, 16-byte aligned; in_stride a multiple of 8. */
+int ds4a_quantize_mxfp4(int n_rows, int K, const ds4a_bf16* in, int64_t in_stride, uint8_t* codes,
+                        uint8_t* scales, ds4a_stream stream);
+
+/* Bytes of workspace ds4a_out_proj_mxfp4 needs (0: bad arguments). */
+size_t ds4a_out_proj_mxfp4_workspace(const ds4a_oproj_cfg* cfg, int M);
+
+/*
+ * ds4a_out_proj_mxfp4 -- ds4a_out_proj with both products in microscaled
+ * 4-bit floating point: the attention output and the intermediate are
+ * quantised on the way (the intermediate from its float32 sums), products
+ * accumulate in float32, y is bf16.
+ *   mid4[t]  = MX4(W_a[j] . MX4(o[t])_j)_j,   y[t] = W_b . mid4[t]
+ *
+ *   wa_codes, wa_scales   the g * r rows of the groups, one after another,
+ *                         K = (H/g) * D
+ *   wb_codes, wb_scales   hidden rows, K = g * r
+ * (H/g)*D, r and hidden must be multiples of 256 (DS4A_EUNSUPPORTED
+ * otherwise).  A block of o that holds a NaN or an infinity gives values that
+ * are not specified, in its own row of y only.
+ */
+int ds4a_out_proj_mxfp4(const ds4a_oproj_cfg* cfg, int M, const ds4a_bf16* o, const uint8_t* wa_codes,
+                        const uint8_t* wa_scales, const uint8_t* wb_codes, const uint8_t* wb_scales, ds4a_bf16* y,
+                        void* ws, size_t ws_bytes, ds4a_stream stream);
+
 /* Synchronise the stream, then read and clear the current device's error
  * word.  Returns DS4A_OK, DS4A_EDEVICE (bad index / position),
  * DS4A_ETIMEOUT (a bounded wait ran out) or DS4A_ECUDA (a CUDA error is

@@ -2,6 +2,9 @@
 // dispatch to the kernels, the device error word and the launch trace.
 #include "ds4a_internal.cuh"
 #include "ds4a_mx.cuh"
+#include "ds4a_evict.cuh"
+#include "ds4a_mxfp4.cuh"
+#include "ds4a_paged.cuh"
 
 #include <math.h>
 #include <stdio.h>
@@ -156,6 +159,7 @@ int ds4a_compress(const ds4a_layer_cfg* cfg, int B, int T_tok, int tok_begin, in
   a.bias_a = bias_a; a.bias_b = bias_b; a.norm_g = norm_g;
   a.entry_begin = entry_begin; a.entry_end = entry_end;
   a.pool = pool; a.pool_bstride = pool_bstride;
+  a.pg_table = nullptr;
   a.app_pos = nullptr; a.ring = nullptr; a.ring_cap = 0; a.n_cap = 0;
   a.qfmt = 0; a.qpool = nullptr; a.q_bstride = 0; a.q_row = 0; a.qscales = nullptr; a.qs_bstride = 0;
   fill_rope_theta(&a.rope, a.rope_dim, cfg->rope_base);
@@ -216,6 +220,7 @@ static int build_append_args(const ds4a_layer_cfg* cfg, int B, int c, const int3
   a.bias_a = bias_a; a.bias_b = bias_b; a.norm_g = norm_g;
   a.entry_begin = 0; a.entry_end = 1;
   a.pool = pool; a.pool_bstride = pool_bstride;
+  a.pg_table = nullptr;
   a.app_pos = pos; a.ring = state; a.ring_cap = overlap ? 2 * m : m; a.n_cap = N_cap;
   a.qfmt = qfmt; a.qpool = qpool; a.qscales = qscales;
   a.q_row = qfmt == 1 ? kv_fp8_row_bytes(c, R) : c / 2;
@@ -528,6 +533,236 @@ int ds4a_hca_attend_fp8(const ds4a_layer_cfg* cfg, int B, int T_q, const int32_t
   if (N_c > 0 && !pool) return DS4A_EINVAL;
   return attend_common(cfg, B, T_q, q_pos, q, q_norm_g, nullptr, pool_bstride, N_c, nullptr, win, win_cap,
                        win_bstride, sink, out, ws, ws_bytes, stream, 0, N_c > 0 ? pool : nullptr);
+}
+
+// ---------------------------------------------------------------------------
+// paged cache
+// ---------------------------------------------------------------------------
+// D, R: the row shape (0: the caller does not know it and format decides)
+static int check_kv(const ds4a_paged_kv* kv, int D, int R) {
+  if (!kv || (kv->format != 0 && kv->format != DS4A_MX_KV_FP8)) return DS4A_EINVAL;
+  if (kv->n_pages < 0 || kv->page_size < 1 || kv->max_pages < 0 || kv->table_stride < kv->max_pages) return DS4A_EINVAL;
+  if ((int64_t)kv->max_pages * kv->page_size > (int64_t)1 << 30) return DS4A_EINVAL;
+  if ((int64_t)kv->n_pages * kv->page_size > INT32_MAX) return DS4A_EINVAL;
+  if (kv->max_pages > 0 && (!kv->table || (kv->n_pages > 0 && !kv->pages))) return DS4A_EINVAL;
+  if (!aligned16(kv->pages) || (reinterpret_cast<uintptr_t>(kv->table) & 3u)) return DS4A_EINVAL;
+  if (kv->format == DS4A_MX_KV_FP8 && ds4a_kv_fp8_row_bytes(D, R) == 0) return DS4A_EUNSUPPORTED;
+  return DS4A_OK;
+}
+
+static int paged_row_bytes(const ds4a_layer_cfg* cfg, const ds4a_paged_kv* kv) {
+  return kv->format ? kv_fp8_row_bytes(cfg->head_dim, cfg->rope_dim) : 2 * cfg->head_dim;
+}
+
+// shape and schedule of a call, and its workspace from `ws` on (nullptr: only
+// the size is wanted)
+static size_t paged_layout(const ds4a_layer_cfg* cfg, const ds4a_paged_kv* kv, int B, int sparse, int weights, void* ws,
+                           PagedArgs* a) {
+  a->B = B; a->H = cfg->n_heads; a->D = cfg->head_dim; a->R = cfg->rope_dim; a->W = cfg->window;
+  a->m = cfg->ratio; a->k = cfg->topk; a->cap = kv->max_pages * kv->page_size; a->sparse = sparse;
+  paged_shape_generic(a);
+  a->hgroups = (a->H + a->hn - 1) / a->hn;
+  const int64_t keys = (int64_t)(sparse ? min(a->k, a->cap) : a->cap) + a->W;
+  const int64_t items = (int64_t)B * a->hgroups, tiles = items * ((keys + a->kt - 1) / a->kt);
+  if (tiles > INT32_MAX) return 0;
+  a->G = (int)(tiles < a->G ? (tiles > 0 ? tiles : 1) : a->G);
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    unsigned char* p = ws ? static_cast<unsigned char*>(ws) + at : nullptr;
+    at += (bytes + 255) / 256 * 256;
+    return p;
+  };
+  a->first = reinterpret_cast<int32_t*>(take((size_t)(items + 1) * 4));
+  a->part = reinterpret_cast<float*>(take((size_t)2 * a->G * (2 * a->hn + (size_t)a->hn * a->D) * 4));
+  a->whole_ml = a->tile_ref = nullptr;
+  a->tile_p = nullptr;
+  if (weights) {
+    a->whole_ml = reinterpret_cast<float*>(take((size_t)items * 2 * a->hn * 4));
+    a->tile_ref = reinterpret_cast<float*>(take((size_t)tiles * a->hn * 4));
+    a->tile_p = reinterpret_cast<uint16_t*>(take((size_t)tiles * a->kt * a->hn * 2));
+  }
+  return at;
+}
+
+size_t ds4a_paged_attend_workspace(const ds4a_layer_cfg* cfg, const ds4a_paged_kv* kv, int B, int sparse,
+                                   int weights) {
+  if (check_cfg(cfg) != DS4A_OK || B <= 0 || check_kv(kv, cfg->head_dim, cfg->rope_dim) != DS4A_OK) return 0;
+  PagedArgs a;
+  return paged_layout(cfg, kv, B, sparse != 0, weights != 0, nullptr, &a);
+}
+
+int ds4a_paged_attend(const ds4a_layer_cfg* cfg, const ds4a_paged_kv* kv, int B, const int32_t* q_pos,
+                      const ds4a_bf16* q, const float* q_norm_g, const int32_t* drop, const int32_t* idx,
+                      const ds4a_bf16* win, int win_cap, int64_t win_bstride, const float* sink, ds4a_bf16* out,
+                      ds4a_bf16* weights, int w_len, int64_t w_stride, void* ws, size_t ws_bytes,
+                      ds4a_stream stream) {
+  if (check_cfg(cfg) != DS4A_OK) return DS4A_EINVAL;
+  if (const int rc = check_kv(kv, cfg->head_dim, cfg->rope_dim)) return rc;
+  const int D = cfg->head_dim;
+  if (B < 0 || B > 65535 || (idx && (cfg->topk < 1 || cfg->topk > 4096))) return DS4A_EINVAL;
+  if (B == 0) return DS4A_OK;
+  if (!q_pos || !q || !q_norm_g || !sink || !out) return DS4A_EINVAL;
+  if (cfg->window > 0 && (!win || win_cap < cfg->window || win_bstride < (int64_t)win_cap * D || win_bstride % 8 != 0))
+    return DS4A_EINVAL;
+  if (!aligned16(q_pos) || !aligned16(q) || !aligned16(q_norm_g) || !aligned16(sink) || !aligned16(out) ||
+      !aligned16(win) || !aligned16(idx) || !aligned16(drop) || !aligned16(weights) || !aligned16(ws))
+    return DS4A_EINVAL;
+  if (weights && idx) return DS4A_EUNSUPPORTED;
+  if (weights && (w_len < 0 || w_stride < w_len)) return DS4A_EINVAL;
+  PagedArgs a;
+  const size_t need = paged_layout(cfg, kv, B, idx != nullptr, weights != nullptr, ws, &a);
+  if (need == 0) return DS4A_EINVAL;
+  if (!ws || ws_bytes < need) return DS4A_ENOSPACE;
+  a.scale = cfg->sm_scale; a.eps = cfg->rms_eps;
+  a.pages = static_cast<const uint8_t*>(kv->pages);
+  a.fmt = kv->format; a.row_bytes = paged_row_bytes(cfg, kv);
+  a.n_pages = kv->n_pages; a.page_size = kv->page_size; a.table = kv->table; a.table_stride = kv->table_stride;
+  a.drop = drop; a.q_pos = q_pos; a.q = q; a.q_norm_g = q_norm_g; a.idx = idx;
+  a.win = win; a.win_cap = win_cap; a.win_bstride = win_bstride; a.sink = sink; a.out = out;
+  a.weights = weights; a.w_stride = w_stride; a.w_len = w_len;
+  fill_rope_theta(&a.rope, a.R, cfg->rope_base);
+  a.err = err_word();
+  if (!a.err) return DS4A_ECUDA;
+  cudaStream_t s = (cudaStream_t)stream;
+  const cudaError_t e = launch_paged_attend_generic(a, s);
+  return e != cudaSuccess ? DS4A_ECUDA : cuda_rc(launch_paged_join(a, s));
+}
+
+int ds4a_paged_append(const ds4a_layer_cfg* cfg, const ds4a_paged_kv* kv, int B, const int32_t* pos,
+                      const int32_t* drop, const ds4a_bf16* ca, const ds4a_bf16* cb, const ds4a_bf16* za,
+                      const ds4a_bf16* zb, const float* bias_a, const float* bias_b, const float* norm_g,
+                      ds4a_bf16* state, ds4a_stream stream) {
+  if (check_cfg(cfg) != DS4A_OK) return DS4A_EINVAL;
+  const int c = cfg->head_dim, R = norm_g ? cfg->rope_dim : 0;
+  if (const int rc = check_kv(kv, c, R)) return rc;
+  if (!aligned16(drop)) return DS4A_EINVAL;
+  const int fmt = kv->format == DS4A_MX_KV_FP8 ? 1 : 0;
+  // every entry number may come: the slot is checked on the device
+  CompressArgs a;
+  static ds4a_bf16* const kSomePool = reinterpret_cast<ds4a_bf16*>(16);  // never followed: the pages are
+  const int rc = build_append_args(cfg, B, c, pos, ca, cb, za, zb, bias_a, bias_b, norm_g, state, INT32_MAX,
+                                   fmt ? nullptr : kSomePool, INT64_MAX - 1, fmt,
+                                   fmt ? reinterpret_cast<uint8_t*>(kSomePool) : nullptr, nullptr, INT32_MAX, &a);
+  if (rc != DS4A_OK || a.B == 0) return rc;
+  a.pool = fmt ? nullptr : static_cast<uint16_t*>(kv->pages);
+  a.qpool = fmt ? static_cast<uint8_t*>(kv->pages) : nullptr;
+  a.pg_table = kv->table; a.pg_stride = kv->table_stride; a.pg_drop = drop;
+  a.pg_size = kv->page_size; a.pg_pages = kv->n_pages; a.pg_cap = kv->max_pages * kv->page_size;
+  return cuda_rc(launch_compress(a, (cudaStream_t)stream));
+}
+
+static size_t evict_ws_bytes(int B, int64_t slots) { return ((size_t)B * 4 + 255) / 256 * 256 + (size_t)B * 2 * slots * 4; }
+
+size_t ds4a_paged_evict_workspace(const ds4a_paged_kv* kv, int B) {
+  if (B <= 0 || check_kv(kv, 0, 0) == DS4A_EINVAL) return 0;
+  return evict_ws_bytes(B, (int64_t)kv->max_pages * kv->page_size);
+}
+
+int ds4a_paged_evict(const ds4a_layer_cfg* cfg, const ds4a_paged_kv* kv, int B, const int32_t* q_pos,
+                     const ds4a_bf16* weights, int64_t w_stride, int budget, int recent, int n_slots, float* acc,
+                     int32_t* entry, int64_t stride, int32_t* drop, void* ws, size_t ws_bytes,
+                     ds4a_stream stream) {
+  if (check_cfg(cfg) != DS4A_OK) return DS4A_EINVAL;
+  if (const int rc = check_kv(kv, cfg->head_dim, cfg->rope_dim)) return rc;
+  const int cap = kv->max_pages * kv->page_size;
+  if (B < 0 || B > 65535 || n_slots < 1 || n_slots > cap || budget < 1 || budget > n_slots || recent < 0 || recent > budget)
+    return DS4A_EINVAL;
+  if (B == 0) return DS4A_OK;
+  if (!q_pos || !acc || !entry || !drop || stride < n_slots || (weights && w_stride < n_slots)) return DS4A_EINVAL;
+  if (!aligned16(q_pos) || !aligned16(weights) || !aligned16(acc) || !aligned16(entry) || !aligned16(drop) ||
+      !aligned16(ws))
+    return DS4A_EINVAL;
+  if (!ws || ws_bytes < evict_ws_bytes(B, cap)) return DS4A_ENOSPACE;
+  EvictArgs a;
+  a.B = B; a.m = cfg->ratio; a.budget = budget; a.recent = recent; a.cap = n_slots;
+  a.pages = static_cast<uint8_t*>(kv->pages); a.row_bytes = paged_row_bytes(cfg, kv);
+  a.n_pages = kv->n_pages; a.page_size = kv->page_size; a.table = kv->table; a.table_stride = kv->table_stride;
+  a.q_pos = q_pos; a.w = weights; a.w_stride = w_stride; a.acc = acc; a.entry = entry; a.stride = stride; a.drop = drop;
+  a.moves = static_cast<int32_t*>(ws);
+  a.list = reinterpret_cast<int32_t*>(static_cast<unsigned char*>(ws) + ((size_t)B * 4 + 255) / 256 * 256);
+  a.err = err_word();
+  if (!a.err) return DS4A_ECUDA;
+  return cuda_rc(launch_evict(a, (cudaStream_t)stream));
+}
+
+// ---------------------------------------------------------------------------
+// microscaled 4-bit products
+// ---------------------------------------------------------------------------
+size_t ds4a_mxfp4_scale_bytes(int rows, int K) {
+  if (rows <= 0 || K <= 0 || K % 128 != 0) return 0;
+  return (size_t)mxfp4_scale_bytes(rows, K);
+}
+
+int ds4a_quantize_mxfp4(int n_rows, int K, const ds4a_bf16* in, int64_t in_stride, uint8_t* codes,
+                        uint8_t* scales, ds4a_stream stream) {
+  if (n_rows < 0 || K <= 0 || K % 128 != 0) return DS4A_EINVAL;
+  if (n_rows == 0) return DS4A_OK;
+  if (!in || !codes || !scales || !aligned16(in) || !aligned16(codes) || !aligned16(scales)) return DS4A_EINVAL;
+  if (in_stride < K || in_stride % 8 != 0) return DS4A_EINVAL;
+  return cuda_rc(launch_quantize_mxfp4(n_rows, K, in, false, in_stride, codes, scales, (cudaStream_t)stream));
+}
+
+static int check_oproj_mxfp4(const ds4a_oproj_cfg* c) {
+  if (const int rc = check_oproj(c)) return rc;
+  const int64_t k1 = (int64_t)(c->n_heads / c->n_groups) * c->head_dim;
+  if (k1 % 256 != 0 || k1 * c->n_groups > (1 << 20)) return DS4A_EUNSUPPORTED;
+  return DS4A_OK;
+}
+
+// quantised o, float intermediate, its quantised form
+struct OprojMxfp4Ws {
+  uint8_t *o_codes, *o_scales, *mid_codes, *mid_scales;
+  float* mid;
+};
+static size_t oproj_mxfp4_layout(const ds4a_oproj_cfg* c, int M, void* ws, OprojMxfp4Ws* w) {
+  const int64_t k = (int64_t)c->n_heads * c->head_dim, n1 = (int64_t)c->n_groups * c->group_rank;
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    unsigned char* p = ws ? static_cast<unsigned char*>(ws) + at : nullptr;
+    at += (bytes + 255) / 256 * 256;
+    return p;
+  };
+  w->o_codes = take((size_t)M * k / 2);
+  w->o_scales = take((size_t)mxfp4_scale_bytes(M, k));
+  w->mid_codes = take((size_t)M * n1 / 2);
+  w->mid_scales = take((size_t)mxfp4_scale_bytes(M, n1));
+  w->mid = reinterpret_cast<float*>(take((size_t)M * n1 * 4));
+  return at;
+}
+
+size_t ds4a_out_proj_mxfp4_workspace(const ds4a_oproj_cfg* cfg, int M) {
+  if (check_oproj_mxfp4(cfg) != DS4A_OK || M <= 0) return 0;
+  OprojMxfp4Ws w;
+  return oproj_mxfp4_layout(cfg, M, nullptr, &w);
+}
+
+int ds4a_out_proj_mxfp4(const ds4a_oproj_cfg* cfg, int M, const ds4a_bf16* o, const uint8_t* wa_codes,
+                        const uint8_t* wa_scales, const uint8_t* wb_codes, const uint8_t* wb_scales, ds4a_bf16* y,
+                        void* ws, size_t ws_bytes, ds4a_stream stream) {
+  if (const int rc = check_oproj_mxfp4(cfg)) return rc;
+  if (M < 0) return DS4A_EINVAL;
+  if (M == 0) return DS4A_OK;
+  if (!o || !wa_codes || !wa_scales || !wb_codes || !wb_scales || !y) return DS4A_EINVAL;
+  if (!aligned16(o) || !aligned16(wa_codes) || !aligned16(wa_scales) || !aligned16(wb_codes) || !aligned16(wb_scales) ||
+      !aligned16(y) || !aligned16(ws))
+    return DS4A_EINVAL;
+  OprojMxfp4Ws w;
+  if (!ws || ws_bytes < oproj_mxfp4_layout(cfg, M, ws, &w)) return DS4A_ENOSPACE;
+  const int k = cfg->n_heads * cfg->head_dim, k1 = k / cfg->n_groups, n1 = cfg->n_groups * cfg->group_rank;
+  cudaStream_t s = (cudaStream_t)stream;
+  unsigned int* err = err_word();
+  if (!err) return DS4A_ECUDA;
+  if (launch_quantize_mxfp4(M, k, o, false, k, w.o_codes, w.o_scales, s) != cudaSuccess) return DS4A_ECUDA;
+  Mxfp4Product p;
+  p.M = M; p.N = n1; p.K = k1; p.n_per_group = cfg->group_rank; p.a_cols = k;
+  p.a_codes = w.o_codes; p.a_scales = w.o_scales; p.b_codes = wa_codes; p.b_scales = wa_scales;
+  p.y = nullptr; p.mid = w.mid; p.err = err;
+  if (launch_mxfp4_product(p, s) != cudaSuccess) return DS4A_ECUDA;
+  if (launch_quantize_mxfp4(M, n1, w.mid, true, n1, w.mid_codes, w.mid_scales, s) != cudaSuccess) return DS4A_ECUDA;
+  p.N = cfg->hidden; p.K = n1; p.n_per_group = cfg->hidden; p.a_cols = n1;
+  p.a_codes = w.mid_codes; p.a_scales = w.mid_scales; p.b_codes = wb_codes; p.b_scales = wb_scales;
+  p.y = y; p.mid = nullptr;
+  return cuda_rc(launch_mxfp4_product(p, s));
 }
 
 int ds4a_check(ds4a_stream stream, uint32_t* bits_out) {

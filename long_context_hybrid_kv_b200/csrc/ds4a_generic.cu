@@ -74,9 +74,21 @@ __device__ __forceinline__ const uint16_t* term_row(const CompressArgs& a, bool 
   return a.ring + (((int64_t)b * S + st) * a.ring_cap + (tok % a.ring_cap)) * a.c;
 }
 
+// Paged output: the row of entry i of sequence b among all pages' rows, or -1
+// (a slot outside the table or a bad page).
+__device__ __forceinline__ int64_t page_row(const CompressArgs& a, int b, int i) {
+  const int slot = i - (a.pg_drop ? a.pg_drop[b] : 0);
+  if (slot < 0 || slot >= a.pg_cap) return -1;
+  const int pg = slot / a.pg_size, ph = a.pg_table[(int64_t)b * a.pg_stride + pg];
+  if (ph < 0 || ph >= a.pg_pages) return -1;
+  return (int64_t)ph * a.pg_size + (slot - pg * a.pg_size);
+}
+
 // Append mode: the entry that sequence b's new token (position p) closes,
 // or -1 (no entry closes, a bad position, or an entry past the pool).
-__device__ __forceinline__ int closing_entry(const CompressArgs& a, int p, bool report) {
+// *row: the entry's row among the pages (paged output only; looked up here
+// once, so that what was checked is what is written).
+__device__ __forceinline__ int closing_entry(const CompressArgs& a, int b, int p, bool report, int64_t* row) {
   if (p < 0) {
     if (report) raise_err(a.err, DS4A_DEV_BAD_POS);
     return -1;
@@ -87,7 +99,24 @@ __device__ __forceinline__ int closing_entry(const CompressArgs& a, int p, bool 
     if (report) raise_err(a.err, DS4A_DEV_BAD_INDEX);
     return -1;
   }
+  if (a.pg_table != nullptr) {
+    *row = page_row(a, b, i);
+    if (*row < 0) {
+      if (report) raise_err(a.err, DS4A_DEV_BAD_INDEX);
+      return -1;
+    }
+  }
   return i;
+}
+
+// First element of entry i of sequence b in the bf16 pool, and its byte row
+// in a block-scaled one (row: as closing_entry gave it).
+__device__ __forceinline__ uint16_t* entry_dst(const CompressArgs& a, int b, int i, int64_t row) {
+  return a.pool + (a.pg_table != nullptr ? row * a.c : (int64_t)b * a.pool_bstride + (int64_t)i * a.c);
+}
+__device__ __forceinline__ uint8_t* entry_dst_mx(const CompressArgs& a, int b, int i, int64_t row) {
+  return a.qpool +
+         (a.pg_table != nullptr ? row * a.q_row : (int64_t)b * a.q_bstride + (int64_t)i * a.q_row);
 }
 
 // Append mode: store the new token's rows of every stream (position p >= 0)
@@ -120,8 +149,8 @@ __device__ __forceinline__ void append_token(const CompressArgs& a, int b, int p
 // the block-scaled case every lane of the warp calls it, the warp holding 64
 // consecutive channels that start at a multiple of 64 (two 32-channel
 // blocks, one per half-warp).
-__device__ __forceinline__ void store_entry_pair(const CompressArgs& a, int b, int i, int ch, float x0, float x1,
-                                                 uint16_t* dst) {
+__device__ __forceinline__ void store_entry_pair(const CompressArgs& a, int b, int i, int64_t prow, int ch, float x0,
+                                                 float x1, uint16_t* dst) {
   const unsigned int packed = f2_to_bf2x2(x0, x1);
   if (a.qfmt == 0) {
     *reinterpret_cast<unsigned int*>(dst) = packed;
@@ -133,7 +162,7 @@ __device__ __forceinline__ void store_entry_pair(const CompressArgs& a, int b, i
   for (int o = 1; o < 16; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
   const bool lead = (threadIdx.x & 15) == 0;
   if (a.qfmt == 1) {
-    uint8_t* row = a.qpool + (int64_t)b * a.q_bstride + (int64_t)i * a.q_row;
+    uint8_t* row = entry_dst_mx(a, b, i, prow);
     const int R = a.rope_dim, n = a.c - R;
     if (ch >= n) {  // RoPE dims stay bf16
       *reinterpret_cast<unsigned int*>(row + n + 2 * (ch - n)) = packed;
@@ -171,10 +200,11 @@ __device__ __forceinline__ void compress_short(const CompressArgs& a) {
   __shared__ float s_red_short[kShortThreads / 32];
   pdl_trigger();
   int i = a.entry_begin + blockIdx.x, newtok = -1;
+  int64_t prow = -1;
   if (a.app_pos != nullptr) {
     pdl_wait();
     newtok = a.app_pos[b];
-    i = closing_entry(a, newtok, tid == 0);
+    i = closing_entry(a, b, newtok, tid == 0, &prow);
     if (i < 0) {
       if (newtok >= 0) append_token(a, b, newtok, tid, kShortThreads);
       return;
@@ -232,9 +262,9 @@ __device__ __forceinline__ void compress_short(const CompressArgs& a) {
   }
   if (a.app_pos == nullptr) pdl_wait();  // a preceding kernel may still read the entry this one overwrites
   if (ch >= c) return;
-  uint16_t* dst = a.qfmt ? nullptr : a.pool + (int64_t)b * a.pool_bstride + (int64_t)i * c + ch;
+  uint16_t* dst = a.qfmt ? nullptr : entry_dst(a, b, i, prow) + ch;
   if (a.norm_g == nullptr) {
-    store_entry_pair(a, b, i, ch, v0, v1, dst);
+    store_entry_pair(a, b, i, prow, ch, v0, v1, dst);
     return;
   }
   const float rstd = rsqrtf(tot / (float)c + a.eps);
@@ -249,7 +279,7 @@ __device__ __forceinline__ void compress_short(const CompressArgs& a) {
     x0 = y0;
     x1 = y1;
   }
-  store_entry_pair(a, b, i, ch, x0, x1, dst);
+  store_entry_pair(a, b, i, prow, ch, x0, x1, dst);
 }
 
 __global__ void __launch_bounds__(kShortThreads) compress_short_kernel(const __grid_constant__ CompressArgs a) {
@@ -274,10 +304,11 @@ __device__ __forceinline__ void compress_body(const CompressArgs& a) {
   // the entry this one overwrites).  In append mode the ring was written by
   // an earlier call, so everything waits.
   int i = a.entry_begin + blockIdx.x, newtok = -1;
+  int64_t prow = -1;
   if (a.app_pos != nullptr) {
     pdl_wait();
     newtok = a.app_pos[b];
-    i = closing_entry(a, newtok, tid == 0);
+    i = closing_entry(a, b, newtok, tid == 0, &prow);
     if (i < 0) {
       if (newtok >= 0) append_token(a, b, newtok, tid, kCompressThreads);
       return;
@@ -360,12 +391,12 @@ __device__ __forceinline__ void compress_body(const CompressArgs& a) {
     ss += v * v;
   }
   pdl_wait();
-  uint16_t* dst = a.qfmt ? nullptr : a.pool + (int64_t)b * a.pool_bstride + (int64_t)i * c;
+  uint16_t* dst = a.qfmt ? nullptr : entry_dst(a, b, i, prow);
   if (a.norm_g == nullptr) {
     __syncthreads();
     if (a.qfmt) {
       for (int p2 = tid; p2 < c / 2; p2 += kCompressThreads)
-        store_entry_pair(a, b, i, 2 * p2, s_v[2 * p2], s_v[2 * p2 + 1], nullptr);
+        store_entry_pair(a, b, i, prow, 2 * p2, s_v[2 * p2], s_v[2 * p2 + 1], nullptr);
       return;
     }
     for (int ch = tid; ch < c; ch += kCompressThreads) dst[ch] = f2bf(s_v[ch]);
@@ -392,7 +423,7 @@ __device__ __forceinline__ void compress_body(const CompressArgs& a) {
       x0 = y0;
       x1 = y1;
     }
-    store_entry_pair(a, b, i, ch, x0, x1, dst + ch);
+    store_entry_pair(a, b, i, prow, ch, x0, x1, dst + ch);
   }
 }
 
@@ -446,10 +477,11 @@ __global__ void __launch_bounds__(kCompressThreads) compress_split_kernel(Compre
   // Every block of a cluster serves the same sequence, so all of them take
   // the same early exit.
   int i = a.entry_begin + blockIdx.x / Z, newtok = -1;
+  int64_t prow = -1;
   if (a.app_pos != nullptr) {
     pdl_wait();
     newtok = a.app_pos[b];
-    i = closing_entry(a, newtok, zr == 0 && tid == 0);
+    i = closing_entry(a, b, newtok, zr == 0 && tid == 0, &prow);
     if (i < 0) {
       if (zr == 0 && newtok >= 0) append_token(a, b, newtok, tid, kCompressThreads);
       return;
@@ -554,12 +586,12 @@ __global__ void __launch_bounds__(kCompressThreads) compress_split_kernel(Compre
     ss += v * v;
   }
   pdl_wait();
-  uint16_t* dst = a.qfmt ? nullptr : a.pool + (int64_t)b * a.pool_bstride + (int64_t)i * c + ch0;
+  uint16_t* dst = a.qfmt ? nullptr : entry_dst(a, b, i, prow) + ch0;
   if (a.norm_g == nullptr) {
     cl.sync();  // no block leaves while a peer may still read its partials
     if (a.qfmt) {
       for (int p2 = tid; p2 < cz / 2; p2 += kCompressThreads)
-        store_entry_pair(a, b, i, ch0 + 2 * p2, s_v[2 * p2], s_v[2 * p2 + 1], nullptr);
+        store_entry_pair(a, b, i, prow, ch0 + 2 * p2, s_v[2 * p2], s_v[2 * p2 + 1], nullptr);
       return;
     }
     for (int k = tid; k < cz; k += kCompressThreads) dst[k] = f2bf(s_v[k]);
@@ -592,7 +624,7 @@ __global__ void __launch_bounds__(kCompressThreads) compress_split_kernel(Compre
       x0 = y0;
       x1 = y1;
     }
-    store_entry_pair(a, b, i, ch, x0, x1, dst + k);
+    store_entry_pair(a, b, i, prow, ch, x0, x1, dst + k);
   }
 }
 
@@ -646,10 +678,11 @@ __global__ void __cluster_dims__(kChanZ, 1, 1) __launch_bounds__(kChanThreads, 2
   // early exit; in append mode everything waits (the ring is a library
   // output), otherwise only the pool write does
   int i = a.entry_begin + blockIdx.x / kChanZ, newtok = -1;
+  int64_t prow = -1;
   if (a.app_pos != nullptr) {
     pdl_wait();
     newtok = a.app_pos[b];
-    i = closing_entry(a, newtok, zr == 0 && tid == 0);
+    i = closing_entry(a, b, newtok, zr == 0 && tid == 0, &prow);
     if (i < 0) {
       if (zr == 0 && newtok >= 0) append_token(a, b, newtok, tid, kChanThreads);
       return;
@@ -738,9 +771,9 @@ __global__ void __cluster_dims__(kChanZ, 1, 1) __launch_bounds__(kChanThreads, 2
   if (warp != 0) return;
   // warp 0: the block's 64 channels as 32 pairs (a whole 64-channel run, as
   // the block-scaled store wants)
-  uint16_t* dst = a.qfmt ? nullptr : a.pool + (int64_t)b * a.pool_bstride + (int64_t)i * c + ch0;
+  uint16_t* dst = a.qfmt ? nullptr : entry_dst(a, b, i, prow) + ch0;
   if (a.norm_g == nullptr) {
-    if (a.qfmt) store_entry_pair(a, b, i, ch0 + 2 * lane, s_v[2 * lane], s_v[2 * lane + 1], nullptr);
+    if (a.qfmt) store_entry_pair(a, b, i, prow, ch0 + 2 * lane, s_v[2 * lane], s_v[2 * lane + 1], nullptr);
     else *reinterpret_cast<unsigned int*>(dst + 2 * lane) = f2_to_bf2x2(s_v[2 * lane], s_v[2 * lane + 1]);
     return;
   }
@@ -758,7 +791,7 @@ __global__ void __cluster_dims__(kChanZ, 1, 1) __launch_bounds__(kChanThreads, 2
     x0 = y0;
     x1 = y1;
   }
-  store_entry_pair(a, b, i, ch, x0, x1, a.qfmt ? nullptr : dst + k);
+  store_entry_pair(a, b, i, prow, ch, x0, x1, a.qfmt ? nullptr : dst + k);
 }
 
 // whether a job runs in the one-block-per-entry kernel with 8-wide loads

@@ -238,6 +238,12 @@ struct CompressArgs {
   int64_t q_bstride, q_row;
   uint8_t* qscales;
   int64_t qs_bstride;
+  // paged output (pg_table != nullptr, append mode): entry i of sequence b
+  // goes to slot i - pg_drop[b] of its pages, rows counted from pool / qpool
+  const int32_t* pg_table;
+  int64_t pg_stride;
+  const int32_t* pg_drop;  // nullable
+  int pg_size, pg_pages, pg_cap;
   RopeTheta rope;
 };
 cudaError_t launch_compress(const CompressArgs& a, cudaStream_t s);

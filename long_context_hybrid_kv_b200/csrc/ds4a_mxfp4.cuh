@@ -1,0 +1,41 @@
+// Microscaled 4-bit (E2M1 elements, one E8M0 scale per 32 values along K)
+// matrices for products: the layout of their scales, and the launchers.
+//
+// codes   [rows][K / 2] bytes, element 2i in the low nibble
+// scales  blocks of 128 rows x 4 scales (128 values of K), 512 bytes each:
+//         row r, scale j of a block at (r % 32) * 16 + (r / 32) * 4 + j; the
+//         K / 128 blocks of a row range lie side by side.  This is the order
+//         in which the tensor core's scale memory takes them (32 lanes of 16
+//         bytes), so a product copies whole blocks and rearranges nothing.
+#pragma once
+
+#include "ds4a_internal.cuh"
+#include "ds4a_mx.cuh"
+
+namespace ds4a {
+
+__host__ __device__ constexpr int64_t mxfp4_scale_bytes(int64_t rows, int64_t K) {
+  return (rows + 127) / 128 * (K / 128) * 512;
+}
+__host__ __device__ constexpr int64_t mxfp4_scale_at(int64_t row, int64_t block, int64_t K) {
+  return ((row / 128) * (K / 128) + block / 4) * 512 + (row % 32) * 16 + (row % 128) / 32 * 4 + block % 4;
+}
+
+// bf16 (or, f32 set, float) rows -> codes and scales; padding rows of the
+// last block of 128 get zero scales
+cudaError_t launch_quantize_mxfp4(int n_rows, int K, const void* in, bool f32, int64_t in_stride, uint8_t* codes,
+                                  uint8_t* scales, cudaStream_t s);
+
+// One grouped product: outputs n of group j = n / n_per_group take the
+// columns j * k .. (j + 1) * k of A's a_cols.  Either y (bf16 [M][N]) or mid
+// (float [M][N]) is written.
+struct Mxfp4Product {
+  int M, N, K, n_per_group, a_cols;
+  const uint8_t *a_codes, *a_scales, *b_codes, *b_scales;
+  uint16_t* y;
+  float* mid;
+  unsigned int* err;
+};
+cudaError_t launch_mxfp4_product(const Mxfp4Product& p, cudaStream_t s);
+
+}  // namespace ds4a

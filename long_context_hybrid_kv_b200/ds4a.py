@@ -20,6 +20,9 @@ __all__ = [
     "DS4A_MX_KV_FP8", "DS4A_MX_IDX_FP4", "ds4a_kv_fp8_row_bytes", "ds4a_quantize_kv_fp8", "ds4a_quantize_idx_fp4",
     "ds4a_compress_append_mx", "ds4a_index_topk_fp4", "ds4a_sparse_attend_fp8", "ds4a_hca_attend_fp8",
     "AppendJob", "append_job", "ds4a_compress_append_jobs",
+    "PagedKv", "paged_kv", "ds4a_paged_attend_workspace", "ds4a_paged_attend", "ds4a_paged_append",
+    "ds4a_paged_evict_workspace", "ds4a_paged_evict", "ds4a_mxfp4_scale_bytes", "ds4a_quantize_mxfp4",
+    "ds4a_out_proj_mxfp4_workspace", "ds4a_out_proj_mxfp4",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_lib", "libds4a.so")
@@ -56,6 +59,12 @@ class AppendJob(ctypes.Structure):
                 ("pool_bstride", ctypes.c_int64)]
 
 
+class PagedKv(ctypes.Structure):
+    _fields_ = [("pages", ctypes.c_void_p), ("table", ctypes.c_void_p), ("table_stride", ctypes.c_int64),
+                ("format", ctypes.c_int32), ("n_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("max_pages", ctypes.c_int32)]
+
+
 def layer_cfg(c) -> LayerCfg:
     """LayerCfg from any object with the fields of ds4a_layer_cfg
     (sm_scale defaults to 1/sqrt(head_dim))."""
@@ -70,6 +79,7 @@ _I = ctypes.c_int
 _I64 = ctypes.c_int64
 _SZ = ctypes.c_size_t
 _CFG = ctypes.POINTER(LayerCfg)
+_KV = ctypes.POINTER(PagedKv)
 
 _SIGS = {
     "ds4a_compress": (_I, [_CFG, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P, _I, _I, _P, _I64, _P]),
@@ -97,6 +107,15 @@ _SIGS = {
     "ds4a_trace_enable": (_I, [_I]),
     "ds4a_trace_read": (_I, [ctypes.POINTER(ctypes.c_char_p), ctypes.POINTER(ctypes.c_float), _I]),
     "ds4a_version": (_I, []),
+    "ds4a_paged_attend_workspace": (_SZ, [_CFG, _KV, _I, _I, _I]),
+    "ds4a_paged_attend": (_I, [_CFG, _KV, _I, _P, _P, _P, _P, _P, _P, _I, _I64, _P, _P, _P, _I, _I64, _P, _SZ, _P]),
+    "ds4a_paged_append": (_I, [_CFG, _KV, _I, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P]),
+    "ds4a_paged_evict_workspace": (_SZ, [_KV, _I]),
+    "ds4a_paged_evict": (_I, [_CFG, _KV, _I, _P, _P, _I64, _I, _I, _I, _P, _P, _I64, _P, _P, _SZ, _P]),
+    "ds4a_mxfp4_scale_bytes": (_SZ, [_I, _I]),
+    "ds4a_quantize_mxfp4": (_I, [_I, _I, _P, _I64, _P, _P, _P]),
+    "ds4a_out_proj_mxfp4_workspace": (_SZ, [ctypes.POINTER(OprojCfg), _I]),
+    "ds4a_out_proj_mxfp4": (_I, [ctypes.POINTER(OprojCfg), _I, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]),
 }
 
 
@@ -343,6 +362,138 @@ def ds4a_out_proj(cfg: OprojCfg, o, w_a, w_b, mid, y, ws=None, *, stream=None):
     rc = lib().ds4a_out_proj(ctypes.byref(cfg), M, _ptr(o), _ptr(w_a), _ptr(w_b), _ptr(mid), _ptr(y), _ptr(ws),
                              ws_bytes, _stream(stream))
     _ok(rc, "ds4a_out_proj")
+
+
+def _rows(t, dtype, name, B=None):
+    """A matrix of one row per sequence whose rows are contiguous: (width, stride)."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1) or (B is not None and t.shape[0] != B):
+        raise ValueError(f"{name} must be [{'B' if B is None else B}, n] with contiguous rows")
+    return t.shape[1], (t.stride(0) if t.shape[0] > 1 else max(1, t.shape[1]))
+
+
+def _vec(t, B, name):
+    import torch
+    if t is not None and (t.dtype != torch.int32 or t.shape != (B,) or not t.is_contiguous()):
+        raise ValueError(f"{name} must be contiguous int32 [{B}]")
+    return t
+
+
+def paged_kv(pages, table, page_size: int, *, fmt: int = 0) -> PagedKv:
+    """The paged cache of ds4a_paged_*: pages [n_pages, page_size, D] bf16, or
+    uint8 [n_pages, page_size, row_bytes] with fmt DS4A_MX_KV_FP8; table int32
+    [B, max_pages] (rows may lie apart).  It keeps both tensors alive."""
+    import torch
+    if fmt == 0:
+        _bf16(pages, "pages")
+    elif pages.dtype != torch.uint8 or not pages.is_contiguous():
+        raise ValueError("pages of block-scaled rows must be contiguous uint8")
+    if pages.dim() != 3 or pages.shape[1] != page_size:
+        raise ValueError("pages must be [n_pages, page_size, row]")
+    width, stride = _rows(table, torch.int32, "table")
+    kv = PagedKv(pages.data_ptr(), table.data_ptr(), stride, fmt, pages.shape[0], page_size, width)
+    kv.held = (pages, table)
+    return kv
+
+
+def ds4a_paged_attend_workspace(cfg: LayerCfg, kv: PagedKv, B: int, sparse: bool = False, weights: bool = False) -> int:
+    return lib().ds4a_paged_attend_workspace(ctypes.byref(cfg), ctypes.byref(kv), B, int(bool(sparse)),
+                                             int(bool(weights)))
+
+
+def ds4a_paged_attend(cfg: LayerCfg, kv: PagedKv, q_pos, q, q_norm_g, win, win_cap: int, sink, out, ws, *, drop=None,
+                      idx=None, weights=None, stream=None):
+    """One new token per sequence: q, out [B, H, D], q_pos [B]; idx int32
+    [B, k] selects slots; weights bf16 [B, n] receives each slot's attention."""
+    _bf16(q, "q"), _bf16(out, "out"), _bf16(win, "win")
+    B = q.shape[0]
+    _vec(q_pos, B, "q_pos"), _vec(drop, B, "drop")
+    w_len = w_stride = 0
+    if weights is not None:
+        w_len, w_stride = _rows(weights, q.dtype, "weights", B)
+    rc = lib().ds4a_paged_attend(cfg, kv, B, q_pos.data_ptr(), q.data_ptr(), q_norm_g.data_ptr(), _ptr(drop),
+                                 _ptr(idx), _ptr(win), win_cap, 0 if win is None else win.stride(0), sink.data_ptr(),
+                                 out.data_ptr(), _ptr(weights), w_len, w_stride, _ptr(ws),
+                                 0 if ws is None else ws.numel() * ws.element_size(), _stream(stream))
+    _ok(rc, "ds4a_paged_attend")
+
+
+def ds4a_paged_append(cfg: LayerCfg, kv: PagedKv, pos, ca, za, bias_a, state, *, drop=None, cb=None, zb=None,
+                      bias_b=None, norm_g=None, stream=None):
+    """ds4a_compress_append of new rows [B, D] into a paged cache (slot = entry - drop)."""
+    _bf16(ca, "ca"), _bf16(za, "za"), _bf16(cb, "cb"), _bf16(zb, "zb")
+    B = ca.shape[0]
+    _vec(pos, B, "pos"), _vec(drop, B, "drop")
+    if ca.shape[1] != cfg.head_dim:
+        raise ValueError("a paged cache holds K=V entries of head_dim channels")
+    rc = lib().ds4a_paged_append(cfg, kv, B, _ptr(pos), _ptr(drop), _ptr(ca), _ptr(cb), _ptr(za), _ptr(zb),
+                                 _ptr(bias_a), _ptr(bias_b), _ptr(norm_g), _ptr(state), _stream(stream))
+    _ok(rc, "ds4a_paged_append")
+
+
+def ds4a_paged_evict_workspace(kv: PagedKv, B: int) -> int:
+    return lib().ds4a_paged_evict_workspace(ctypes.byref(kv), B)
+
+
+def ds4a_paged_evict(cfg: LayerCfg, kv: PagedKv, q_pos, budget: int, recent: int, acc, entry, drop, ws, *,
+                     weights=None, stream=None):
+    """acc (float32) += weights (bf16), entry (int32), all [B, n_slots]; caches
+    of more than budget entries are cut to it in place, drop [B] follows."""
+    import torch
+    B = q_pos.shape[0]
+    _vec(q_pos, B, "q_pos"), _vec(drop, B, "drop")
+    n, stride = _rows(acc, torch.float32, "acc", B)
+    if _rows(entry, torch.int32, "entry", B) != (n, stride):
+        raise ValueError("acc and entry must have the same shape and stride")
+    w_stride = 0
+    if weights is not None:
+        w_len, w_stride = _rows(weights, torch.bfloat16, "weights", B)
+        if w_len < n:
+            raise ValueError("weights must cover the slots of acc")
+    rc = lib().ds4a_paged_evict(cfg, kv, B, q_pos.data_ptr(), _ptr(weights), w_stride, budget, recent, n,
+                                acc.data_ptr(), entry.data_ptr(), stride, drop.data_ptr(), _ptr(ws),
+                                0 if ws is None else ws.numel() * ws.element_size(), _stream(stream))
+    _ok(rc, "ds4a_paged_evict")
+
+
+def ds4a_mxfp4_scale_bytes(rows: int, K: int) -> int:
+    return lib().ds4a_mxfp4_scale_bytes(rows, K)
+
+
+def _u8(t, n, name):
+    import torch
+    if t.dtype != torch.uint8 or not t.is_contiguous() or t.numel() < n:
+        raise ValueError(f"{name} must be contiguous uint8 of at least {n} bytes")
+    return t.data_ptr()
+
+
+def ds4a_quantize_mxfp4(rows, codes, scales, *, stream=None):
+    """bf16 rows [n, K] (rows may lie apart) -> E2M1 codes [n, K/2] and E8M0
+    scales in the products' order (ds4a_mxfp4_scale_bytes(n, K) bytes)."""
+    import torch
+    n, K = rows.shape
+    if rows.dtype != torch.bfloat16 or (K > 1 and rows.stride(1) != 1):
+        raise ValueError("rows must be bfloat16 [n, K] with contiguous rows")
+    rc = lib().ds4a_quantize_mxfp4(n, K, _ptr(rows), rows.stride(0) if n > 1 else K, _u8(codes, n * K // 2, "codes"),
+                                   _u8(scales, ds4a_mxfp4_scale_bytes(n, K), "scales"), _stream(stream))
+    _ok(rc, "ds4a_quantize_mxfp4")
+
+
+def ds4a_out_proj_mxfp4_workspace(cfg: OprojCfg, M: int) -> int:
+    return lib().ds4a_out_proj_mxfp4_workspace(ctypes.byref(cfg), M)
+
+
+def ds4a_out_proj_mxfp4(cfg: OprojCfg, o, wa_codes, wa_scales, wb_codes, wb_scales, y, ws, *, stream=None):
+    """o [M, H, D] -> y [M, hidden], weights and activations in MXFP4."""
+    _bf16(o, "o"), _bf16(y, "y")
+    n1, k1 = cfg.n_groups * cfg.group_rank, cfg.n_heads // max(1, cfg.n_groups) * cfg.head_dim
+    rc = lib().ds4a_out_proj_mxfp4(cfg, o.shape[0], o.data_ptr(), _u8(wa_codes, n1 * k1 // 2, "wa_codes"),
+                                   _u8(wa_scales, n1 * k1 // 32, "wa_scales"),
+                                   _u8(wb_codes, cfg.hidden * n1 // 2, "wb_codes"),
+                                   _u8(wb_scales, cfg.hidden * n1 // 32, "wb_scales"), y.data_ptr(), _ptr(ws),
+                                   0 if ws is None else ws.numel() * ws.element_size(), _stream(stream))
+    _ok(rc, "ds4a_out_proj_mxfp4")
 
 
 def ds4a_check(stream=None) -> tuple[int, int]:
