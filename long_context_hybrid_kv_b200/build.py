@@ -16,7 +16,7 @@ OUT = os.path.join(PKG, "_lib", "libds4a.so")
 BUILD = os.path.join(ROOT, "_build", "ds4a")
 
 SOURCES = ["ds4a_api.cu", "ds4a_generic.cu", "ds4a_index_tc.cu", "ds4a_attend_tc.cu", "ds4a_noalloc.cu", "ds4a_topk.cu",
-           "ds4a_selftest.cu", "ds4a_outproj.cu", "ds4a_mx.cu", "ds4a_paged.cu", "ds4a_evict.cu", "ds4a_mxfp4.cu"]
+           "ds4a_selftest.cu", "ds4a_outproj.cu", "ds4a_mx.cu", "ds4a_paged.cu", "ds4a_paged_tc.cu", "ds4a_evict.cu", "ds4a_mxfp4.cu"]
 HEADERS = ["ds4a_internal.cuh", "ds4a_tc.cuh", "ds4a_mx.cuh", "ds4a_paged.cuh", "ds4a_evict.cuh", "ds4a_mxfp4.cuh"]
 
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")

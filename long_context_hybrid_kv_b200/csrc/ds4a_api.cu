@@ -560,7 +560,9 @@ static size_t paged_layout(const ds4a_layer_cfg* cfg, const ds4a_paged_kv* kv, i
                            PagedArgs* a) {
   a->B = B; a->H = cfg->n_heads; a->D = cfg->head_dim; a->R = cfg->rope_dim; a->W = cfg->window;
   a->m = cfg->ratio; a->k = cfg->topk; a->cap = kv->max_pages * kv->page_size; a->sparse = sparse;
-  paged_shape_generic(a);
+  // rows of 512 run on the tensor cores, other shapes on the CUDA cores
+  if (paged_tc_supported(*a, kv->format)) paged_shape_tc(a);
+  else paged_shape_generic(a);
   a->hgroups = (a->H + a->hn - 1) / a->hn;
   const int64_t keys = (int64_t)(sparse ? min(a->k, a->cap) : a->cap) + a->W;
   const int64_t items = (int64_t)B * a->hgroups, tiles = items * ((keys + a->kt - 1) / a->kt);
@@ -624,7 +626,7 @@ int ds4a_paged_attend(const ds4a_layer_cfg* cfg, const ds4a_paged_kv* kv, int B,
   a.err = err_word();
   if (!a.err) return DS4A_ECUDA;
   cudaStream_t s = (cudaStream_t)stream;
-  const cudaError_t e = launch_paged_attend_generic(a, s);
+  const cudaError_t e = paged_tc_supported(a, a.fmt) ? launch_paged_attend_tc(a, s) : launch_paged_attend_generic(a, s);
   return e != cudaSuccess ? DS4A_ECUDA : cuda_rc(launch_paged_join(a, s));
 }
 

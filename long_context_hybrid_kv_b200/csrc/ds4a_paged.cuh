@@ -177,9 +177,12 @@ __device__ __forceinline__ PagedRange paged_range(const PagedArgs& a, int c) {
   return r;
 }
 
-// head group, tile and grid of the CUDA-core kernel
+// head group, tile and grid of the two kernels
 void paged_shape_generic(PagedArgs* a);
+void paged_shape_tc(PagedArgs* a);
+bool paged_tc_supported(const PagedArgs& a, int fmt);
 cudaError_t launch_paged_attend_generic(const PagedArgs& a, cudaStream_t s);
+cudaError_t launch_paged_attend_tc(const PagedArgs& a, cudaStream_t s);
 cudaError_t launch_paged_join(const PagedArgs& a, cudaStream_t s);
 
 }  // namespace ds4a

@@ -1,0 +1,686 @@
+// Decode attention over a paged K=V cache on the tensor cores (tcgen05), for
+// rows of 512: "DeepSeek-v4 Beyond Basics" 3.2.2 eq. 19 and 3.3 eqs. 24-27 for
+// one new token per sequence; schedule in ds4a_paged.cuh.
+//
+// All heads read the same rows, so a tile of 96 keys is two dense products with
+// the keys, then the dims, on the MMA's M side and 64 heads on N:
+//   S^T[key][h]  = KV[key][:] . q^[h][:]      K = 512, A K-major, M = 128
+//   O^T[d][h]   += KV[key][d]^T . P^T[key][h]  K = 96 keys, A MN-major
+// M = 128 reads 32 rows past the tile's 96 (whatever lies behind them in
+// shared memory); an A row only reaches its own row of S^T, and those are not
+// looked at.  96 keys instead of 128 leave room for one and a half tiles next
+// to the 64 KiB of q^: the next tile's rows arrive, and half of its first
+// product runs, during this tile's softmax.  By 44 GB/s of HBM an SM a tile
+// takes 2.2 us, its products 1.4 us (N = 64 is bound by the 6 KiB of shared
+// memory an MMA reads), so that the loads are to be kept going.
+//
+// Thread block (one per SM, 512 threads):
+//   warps 0-7    q^ of every segment, softmax, epilogue: two warps per TMEM
+//                lane quarter with 32 heads each; thread = key row of S^T,
+//                later dim row of O^T (the last quarter holds no keys).
+//   warp 8       TMEM allocation; lane 0 issues the MMAs.
+//   warps 9-12   gather the rows by cp.async, 128 dims (24 KiB) at a time,
+//                into a ring of six such slots, in the 128-byte swizzle.  FP8
+//                rows go through registers and are expanded on the way.
+//   warps 13-15  one key a thread, up to four tiles ahead: index, page, row
+//                address, and a prefetch of the row into L2, so that HBM keeps
+//                streaming while the ring is full.
+#include "ds4a_paged.cuh"
+#include "ds4a_tc.cuh"
+
+namespace ds4a {
+namespace {
+
+using namespace tc;
+
+constexpr int kH = 64, kD = 512;
+constexpr int kKT = 96;               // keys per tile
+constexpr int kThreads = 512;
+constexpr int kMmaWarp = 8;
+constexpr int kPG0 = 288;             // first gathering thread (warps 9-12)
+constexpr int kPtr0 = 416;            // first address thread (warps 13-15)
+constexpr int kSlots = 6;             // ring of 128-dim chunks
+constexpr int kAhead = 4;             // tiles of row addresses
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kRescaleLog2 = 8.0f;  // O^T is rescaled when a head's maximum grows by more than 2^8
+constexpr float kNoRef = -1e30f;      // reference of a head that has seen no key: finite, below any logit
+
+constexpr uint32_t kBlk = kKT * 128;   // 64 dims of a tile's keys
+constexpr uint32_t kSlot = 2 * kBlk;   // 128 dims
+constexpr uint32_t kOffKV = 0;
+constexpr uint32_t kOffQ = kSlots * kSlot;       // 8 blocks x [64 heads][128 B]
+constexpr uint32_t kOffP = kOffQ + 65536;        // [96 keys][128 B]
+constexpr uint32_t kOffBar = kOffP + kBlk;
+constexpr uint32_t kOffMisc = kOffBar + 256;     // abort flag, TMEM address, the block's range
+constexpr uint32_t kOffRow = kOffMisc + 64;      // [4 tiles][96] row addresses, bit 0: FP8
+constexpr uint32_t kOffRed = kOffRow + kAhead * kKT * 8;  // [4][64] floats
+constexpr uint32_t kOffMrun = kOffRed + 1024;
+constexpr uint32_t kOffAlpha = kOffMrun + 256;
+constexpr uint32_t kOffInv = kOffAlpha + 256;
+constexpr uint32_t kOffSink = kOffInv + 256;
+constexpr uint32_t kOffValid = kOffSink + 256;   // [2 tiles][96]
+constexpr uint32_t kSmemBytes = kOffValid + 2 * kKT + 1024;
+static_assert(kSmemBytes <= 232448, "shared memory of a block");
+// The finished output goes out through the q^ and P^T buffers, a head's 1024
+// bytes 1088 apart (the two heads that a warp writes at a time then lie in
+// different banks).
+constexpr uint32_t kStagePitch = 1088;
+static_assert(kH * kStagePitch <= 65536 + kBlk, "output stage");
+
+enum Bar {
+  kKVFull = 0, kKVEmpty = kKVFull + kSlots, kRowFull = kKVEmpty + kSlots, kRowEmpty = kRowFull + kAhead,
+  kQFull = kRowEmpty + kAhead, kSFull, kPFull, kPVDone, kEpiDone, kDrain, kNumBars
+};
+static_assert(kNumBars * 8 <= 256, "barriers");
+
+constexpr uint32_t kIdescQK = idesc_bf16(128, 64, 0, 0);
+constexpr uint32_t kIdescPV = idesc_bf16(128, 64, 1, 1);
+
+// smem -> global, 16-byte aligned, in the thread's bulk group
+__device__ __forceinline__ void bulk_s2g(void* dst, uint32_t src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src), "r"(bytes) : "memory");
+}
+
+// The segments of a block one after the other (every role walks them alike).
+struct Walk {
+  int t, t1, item, item_t0, first_item;
+  __device__ __forceinline__ Walk(const PagedRange& r)
+      : t(r.t0), t1(r.t1), item(r.item), item_t0(r.item_t0), first_item(r.item) {}
+};
+struct Segment {
+  int item, b, g, tile0, n_tiles, slot;  // tiles counted in the item; slot of a partial result
+  int t;                                 // first tile in the row of all tiles
+  bool whole;
+  PagedSeq seq;
+};
+__device__ __forceinline__ bool next_segment(const PagedArgs& a, Walk& w, Segment& s) {
+  while (w.t < w.t1) {
+    s.item = w.item;
+    s.b = w.item / a.hgroups;
+    s.g = w.item - s.b * a.hgroups;
+    s.seq = paged_seq(a, s.b);
+    const int n = paged_tiles(a, s.seq), end = w.item_t0 + n;
+    if (w.t >= end) {  // no tiles
+      w.item_t0 = end;
+      ++w.item;
+      continue;
+    }
+    const int stop = min(w.t1, end);
+    s.t = w.t;
+    s.tile0 = w.t - w.item_t0;
+    s.n_tiles = stop - w.t;
+    s.whole = s.n_tiles == n;
+    s.slot = 2 * blockIdx.x + (w.item == w.first_item ? 0 : 1);
+    w.t = stop;
+    w.item_t0 = end;
+    ++w.item;
+    return true;
+  }
+  return false;
+}
+
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+template <bool kFp8>
+__global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __grid_constant__ PagedArgs a) {
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  unsigned char* smem =
+      reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  const uint32_t sbase = smem_u32(smem);
+  const uint32_t kv_base = sbase + kOffKV, q_base = sbase + kOffQ, p_base = sbase + kOffP;
+  auto bar = [&](int i) { return sbase + kOffBar + 8u * (uint32_t)i; };
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kOffMisc);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kOffMisc + 8);
+  PagedRange* s_range = reinterpret_cast<PagedRange*>(smem + kOffMisc + 16);
+  unsigned long long* rows = reinterpret_cast<unsigned long long*>(smem + kOffRow);
+  float* red = reinterpret_cast<float*>(smem + kOffRed);
+  float* mrun = reinterpret_cast<float*>(smem + kOffMrun);
+  float* alpha_s = reinterpret_cast<float*>(smem + kOffAlpha);
+  float* inv_s = reinterpret_cast<float*>(smem + kOffInv);
+  float* sink_s = reinterpret_cast<float*>(smem + kOffSink);
+  uint8_t* vflag = smem + kOffValid;
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  unsigned int* err = a.err;
+
+  pdl_trigger();
+  if (tid == 0) {
+    *abort_flag = 0;
+    for (int i = 0; i < kSlots; ++i) {
+      mbar_init(bar(kKVFull + i), 128);
+      mbar_init(bar(kKVEmpty + i), 1);
+    }
+    for (int i = 0; i < kAhead; ++i) {
+      mbar_init(bar(kRowFull + i), kKT);
+      mbar_init(bar(kRowEmpty + i), 128);
+    }
+    mbar_init(bar(kQFull), 256);
+    mbar_init(bar(kSFull), 1);
+    mbar_init(bar(kPFull), 256);
+    mbar_init(bar(kPVDone), 1);
+    mbar_init(bar(kEpiDone), 256);
+    mbar_init(bar(kDrain), 1);
+    fence_barrier_init();
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(smem_u32(tmem_slot), 512);
+    tmem_relinquish();
+  }
+  pdl_wait();
+  if (warp == 0) {
+    const PagedRange r = paged_range(a, blockIdx.x);
+    if (lane == 0) *s_range = r;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  Walk walk(*s_range);
+  Segment sg;
+
+  if (warp < 8) {
+    // =================== q^, softmax, epilogue ===================
+    const int q4 = warp & 3, hf = warp >> 2;
+    const int r = 32 * q4 + lane;  // key row of S^T / dim row of O^T within a chunk
+    const bool has_key = q4 < 3;
+    const int st = tid;            // 0..255
+    const int h0 = 32 * hf;
+    const uint32_t t_lane = tmem + ((uint32_t)(32 * q4) << 16);
+    const float scale2 = a.scale * kLog2e;
+    const int R = a.R;
+    const float4 g0 = *reinterpret_cast<const float4*>(a.q_norm_g + 8 * lane);
+    const float4 g1 = *reinterpret_cast<const float4*>(a.q_norm_g + 8 * lane + 4);
+    const float4 g2 = *reinterpret_cast<const float4*>(a.q_norm_g + 256 + 8 * lane);
+    const float4 g3 = *reinterpret_cast<const float4*>(a.q_norm_g + 256 + 8 * lane + 4);
+    uint32_t gt = 0;
+    while (next_segment(a, walk, sg)) {
+      const int nh = min(kH, a.H - sg.g * kH);
+      const int64_t head0 = (int64_t)sg.b * a.H + sg.g * kH;
+      if (st < kH) {
+        sink_s[st] = st < nh ? a.sink[sg.g * kH + st] * kLog2e : 0.f;
+        mrun[st] = kNoRef;
+      }
+      // q^ = RoPE_pos(RMSNorm(q) g), rounded to bf16 (the MMA's operand), into
+      // the K-major operand layout: warp w takes heads w, w + 8, ..., lane l
+      // dims 8l .. 8l+7 and 256+8l ..; heads that the group does not have are 0
+      {
+        const uint16_t* qrow = a.q + head0 * kD;
+        float rc[4], rs[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          rc[u] = 1.f;
+          rs[u] = 0.f;
+          const int d = 256 + 8 * lane + 2 * u;
+          if (d >= kD - R) rope_cos_sin(sg.seq.pos, a.rope.t[(d - (kD - R)) >> 1], &rc[u], &rs[u]);
+        }
+        const float g[16] = {g0.x, g0.y, g0.z, g0.w, g1.x, g1.y, g1.z, g1.w,
+                             g2.x, g2.y, g2.z, g2.w, g3.x, g3.y, g3.z, g3.w};
+        const uint32_t offA = (uint32_t)(lane >> 3) * 8192u, offB = (uint32_t)(4 + (lane >> 3)) * 8192u;
+#pragma unroll 1
+        for (int h4 = warp; h4 < kH; h4 += 32) {
+          uint4 va[4], vb[4];
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const int h = h4 + 8 * u;
+            va[u] = vb[u] = make_uint4(0, 0, 0, 0);
+            if (h < nh) {
+              va[u] = *reinterpret_cast<const uint4*>(qrow + h * kD + 8 * lane);
+              vb[u] = *reinterpret_cast<const uint4*>(qrow + h * kD + 256 + 8 * lane);
+            }
+          }
+          float ss[4];
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const unsigned int wv[8] = {va[u].x, va[u].y, va[u].z, va[u].w, vb[u].x, vb[u].y, vb[u].z, vb[u].w};
+            float acc = 0.f;
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+              const float2 f = bf2x2_to_f2(wv[q]);
+              acc = fmaf(f.x, f.x, fmaf(f.y, f.y, acc));
+            }
+            ss[u] = acc;
+          }
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+            for (int u = 0; u < 4; ++u) ss[u] += __shfl_xor_sync(0xffffffffu, ss[u], o);
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const int h = h4 + 8 * u;
+            // (a head that is not there: 0 rather than 0 * 1/sqrt(eps))
+            const float rstd = h < nh ? rsqrtf(ss[u] / (float)kD + a.eps) : 0.f;
+            const unsigned int wv[8] = {va[u].x, va[u].y, va[u].z, va[u].w, vb[u].x, vb[u].y, vb[u].z, vb[u].w};
+            uint32_t pq[8];
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+              const float2 f = bf2x2_to_f2(wv[q]);
+              float x0 = f.x * rstd * g[2 * q], x1 = f.y * rstd * g[2 * q + 1];
+              if (q >= 4) {
+                const float y0 = x0 * rc[q - 4] - x1 * rs[q - 4], y1 = x0 * rs[q - 4] + x1 * rc[q - 4];
+                x0 = y0;
+                x1 = y1;
+              }
+              pq[q] = f2_to_bf2x2(x0, x1);
+            }
+            const uint32_t sw = sw128((uint32_t)h, (uint32_t)(lane & 7));
+            st_shared16(q_base + offA + sw, pq[0], pq[1], pq[2], pq[3]);
+            st_shared16(q_base + offB + sw, pq[4], pq[5], pq[6], pq[7]);
+          }
+        }
+        fence_async_smem();
+        mbar_arrive(bar(kQFull));
+      }
+      float lpart[32];
+#pragma unroll
+      for (int i = 0; i < 32; ++i) lpart[i] = 0.f;
+      named_bar(1, 256);
+      for (int tile = 0; tile < sg.n_tiles; ++tile, ++gt) {
+        mbar_wait(bar(kSFull), gt & 1u, abort_flag, err);
+        // the last chunk's barrier (complete before S^T is) orders the
+        // gatherers' flags of this tile before the read
+        mbar_wait(bar(kKVFull + (4 * gt + 3) % kSlots), ((4 * gt + 3) / kSlots) & 1u, abort_flag, err);
+        tc_fence_after();
+        float z[32];
+        float lead = -INFINITY;
+        if (has_key) {
+          // a key slot without a row (zero-filled, so its S^T row is 0) gets
+          // -inf through the bias of the scaling FMA
+          const float zbias = vflag[(gt & 1u) * kKT + r] != 0 ? 0.f : -INFINITY;
+          tmem_ld32(t_lane + (gt & 1u) * 64u + (uint32_t)h0, z);
+          tmem_ld_wait();
+          const float4* mrun4 = reinterpret_cast<const float4*>(mrun + h0);
+          const float2 sc2 = make_float2(scale2, scale2), zb2 = make_float2(zbias, zbias);
+#pragma unroll
+          for (int i4 = 0; i4 < 8; ++i4) {
+            const float4 m4 = mrun4[i4];
+            const float2 za = fma_f2(make_float2(z[4 * i4], z[4 * i4 + 1]), sc2, zb2);
+            const float2 zc = fma_f2(make_float2(z[4 * i4 + 2], z[4 * i4 + 3]), sc2, zb2);
+            z[4 * i4] = za.x;
+            z[4 * i4 + 1] = za.y;
+            z[4 * i4 + 2] = zc.x;
+            z[4 * i4 + 3] = zc.y;
+            const float2 da = sub_f2(za, make_float2(m4.x, m4.y)), dc = sub_f2(zc, make_float2(m4.z, m4.w));
+            lead = fmaxf(lead, fmaxf(fmaxf(da.x, da.y), fmaxf(dc.x, dc.y)));
+          }
+        }
+        const bool rescale = bar_or(1, 256, lead > kRescaleLog2);
+        if (rescale) {
+          if (has_key) red[q4 * 64 + h0 + lane] = warp_reduce32<true>(z);
+          named_bar(1, 256);
+          if (st < kH) {
+            const float mt = fmaxf(fmaxf(red[st], red[64 + st]), red[128 + st]);
+            const float mo = mrun[st];
+            float al = 1.f;
+            if (mt > mo + kRescaleLog2) {  // a -inf tile maximum never moves it
+              al = exp2f(mo - mt);         // 0 from the no-key reference
+              mrun[st] = mt;
+            }
+            alpha_s[st] = al;
+          }
+          named_bar(1, 256);
+          const float4* al4 = reinterpret_cast<const float4*>(alpha_s + h0);
+#pragma unroll
+          for (int i4 = 0; i4 < 8; ++i4) {
+            const float4 a4 = al4[i4];
+            lpart[4 * i4] *= a4.x;
+            lpart[4 * i4 + 1] *= a4.y;
+            lpart[4 * i4 + 2] *= a4.z;
+            lpart[4 * i4 + 3] *= a4.w;
+          }
+        }
+        if (a.weights && st < kH) a.tile_ref[(int64_t)(sg.t + tile) * kH + st] = mrun[st];
+        uint32_t pk[16];
+        if (has_key) {
+#pragma unroll
+          for (int i = 0; i < 32; i += 2) {
+            const float2 m2 = reinterpret_cast<const float2*>(mrun + h0)[i >> 1];
+            // a -inf logit gives 0 (the reference is always finite); P is
+            // rounded to bf16 (the MMA's operand) and summed as rounded
+            const float2 d = sub_f2(make_float2(z[i], z[i + 1]), m2);
+            const uint32_t w2 = f2_to_bf2x2(ex2_approx(d.x), ex2_approx(d.y));
+            pk[i >> 1] = w2;
+            const float2 l2 = add_f2(make_float2(lpart[i], lpart[i + 1]), bf2x2_to_f2(w2));
+            lpart[i] = l2.x;
+            lpart[i + 1] = l2.y;
+          }
+          if (a.weights) {
+            uint4* dst = reinterpret_cast<uint4*>(a.tile_p + ((int64_t)(sg.t + tile) * kKT + r) * kH + h0);
+#pragma unroll
+            for (int cc = 0; cc < 4; ++cc) dst[cc] = make_uint4(pk[4 * cc], pk[4 * cc + 1], pk[4 * cc + 2], pk[4 * cc + 3]);
+          }
+        }
+        if (tile > 0) {
+          // the previous tile's PV must be done before P^T and O^T change
+          mbar_wait(bar(kPVDone), (gt - 1) & 1u, abort_flag, err);
+          tc_fence_after();
+        }
+        if (has_key) {
+#pragma unroll
+          for (int cc = 0; cc < 4; ++cc)
+            st_shared16(p_base + sw128(r, 4 * hf + cc), pk[4 * cc], pk[4 * cc + 1], pk[4 * cc + 2], pk[4 * cc + 3]);
+        }
+        if (tile > 0 && rescale) {
+          const float4* al4 = reinterpret_cast<const float4*>(alpha_s + h0);
+#pragma unroll 1
+          for (int c = 0; c < 8; ++c) {
+            // 16 head columns of one 128-dim chunk at a time
+            float v[16];
+            const uint32_t addr = t_lane + 128u + 64u * (c >> 1) + (uint32_t)h0 + 16u * (c & 1);
+            tmem_ld16(addr, v);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i4 = 0; i4 < 4; ++i4) {
+              const float4 a4 = al4[4 * (c & 1) + i4];
+              v[4 * i4] *= a4.x;
+              v[4 * i4 + 1] *= a4.y;
+              v[4 * i4 + 2] *= a4.z;
+              v[4 * i4 + 3] *= a4.w;
+            }
+            tmem_st16(addr, v);
+          }
+          tmem_st_wait();
+        }
+        fence_async_smem();
+        tc_fence_before();
+        mbar_arrive(bar(kPFull));
+      }
+      // ---------------- epilogue ----------------
+      mbar_wait(bar(kPVDone), (gt - 1) & 1u, abort_flag, err);
+      tc_fence_after();
+      if (has_key) red[q4 * 64 + h0 + lane] = warp_reduce32<false>(lpart);
+      named_bar(1, 256);
+      float* part = a.part + (int64_t)sg.slot * (2 * kH + kH * kD);
+      if (st < kH) {
+        const float l = red[st] + red[64 + st] + red[128 + st];
+        const float m = mrun[st];
+        const float mx = m <= kNoRef ? -INFINITY : m * 0.6931471805599453f;  // natural-log units
+        if (sg.whole) {
+          const float den = m <= kNoRef ? 0.f : l + exp2f(sink_s[st] - m);
+          inv_s[st] = den > 0.f ? 1.f / den : 0.f;
+          if (a.weights) {
+            a.whole_ml[(int64_t)sg.item * 2 * kH + st] = mx;
+            a.whole_ml[(int64_t)sg.item * 2 * kH + kH + st] = l;
+          }
+        } else {
+          part[st] = mx;
+          part[kH + st] = l;
+        }
+      }
+      named_bar(1, 256);
+      const bool odd = r & 1;
+#pragma unroll 1
+      for (int c = 0; c < 4; ++c) {
+        const int d = 128 * c + r;
+        float v[32];
+        tmem_ld32(t_lane + 128u + 64u * c + (uint32_t)h0, v);
+        tmem_ld_wait();
+        if (sg.whole) {
+          // lanes r and r^1 hold dims d and d^1: one exchange per head pair
+          // gives the even lane both dims of the even head and the odd lane
+          // both dims of the odd head, so each lane rotates its pair (rope
+          // slice, by -pos) and writes one 4-byte word of the stage
+          const bool rot = d >= kD - R;
+          float cs = 1.f, sn = 0.f;
+          if (rot) rope_cos_sin(sg.seq.pos, a.rope.t[(d - (kD - R)) >> 1], &cs, &sn);
+          const uint32_t dd = (uint32_t)(d & ~1) * 2u;
+#pragma unroll
+          for (int i = 0; i < 32; i += 2) {
+            const float got = __shfl_xor_sync(0xffffffffu, odd ? v[i] : v[i + 1], 1);
+            const int h = h0 + i + (odd ? 1 : 0);
+            const float s = inv_s[h];
+            float2 x = mul_f2(make_float2(odd ? got : v[i], odd ? v[i + 1] : got), make_float2(s, s));
+            if (rot)  // (x0 cs + x1 sn, -x0 sn + x1 cs)
+              x = fma_f2(make_float2(x.x, x.x), make_float2(cs, -sn), mul_f2(make_float2(x.y, x.y), make_float2(sn, cs)));
+            st_shared32(q_base + (uint32_t)h * kStagePitch + dd, f2_to_bf2x2(x.x, x.y));
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) part[2 * kH + (h0 + i) * kD + d] = v[i];
+        }
+      }
+      tc_fence_before();
+      mbar_arrive(bar(kEpiDone));
+      if (sg.whole) {
+        fence_async_smem();
+        named_bar(1, 256);
+        if (st < nh) {
+          bulk_s2g(a.out + (head0 + st) * kD, q_base + (uint32_t)st * kStagePitch, kD * 2);
+          bulk_commit();
+          bulk_wait_read0();  // the stage is read before the next segment's q^ goes in
+        }
+      }
+      named_bar(1, 256);
+    }
+    if (st < kH) bulk_wait0();
+  } else if (warp == kMmaWarp) {
+    // =================== MMA issuer ===================
+    const uint64_t qk_a0 = sdesc_sw128(kv_base, 16, 1024);
+    const uint64_t qk_b0 = sdesc_sw128(q_base, 16, 1024);
+    const uint64_t pv_a0 = sdesc_sw128(kv_base, kBlk, 1024);
+    const uint64_t pv_b0 = sdesc_sw128(p_base, kBlk, 1024);
+    uint32_t gt = 0, active = 0;
+    while (next_segment(a, walk, sg)) {
+      if (lane == 0) {
+        auto qk_chunk = [&](uint32_t g, int c) {
+          const uint32_t slot = (4 * g + c) % kSlots;
+          const uint32_t d_s = tmem + (g & 1u) * 64u;
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk) {
+            const uint32_t koff = (uint32_t)(kk & 3) * 32u;
+            mma_bf16(d_s, qk_a0 + ((slot * kSlot + (kk >> 2) * kBlk + koff) >> 4),
+                     qk_b0 + (((2u * c + (kk >> 2)) * 8192u + koff) >> 4), kIdescQK, (c | kk) != 0 ? 1u : 0u);
+          }
+        };
+        auto kv_full = [&](uint32_t g, int c) { return bar(kKVFull + (4 * g + c) % kSlots); };
+        auto kv_phase = [&](uint32_t g, int c) { return ((4 * g + c) / kSlots) & 1u; };
+        mbar_wait(bar(kQFull), active & 1u, abort_flag, err);
+        tc_fence_after();
+        int qc = 0;
+        for (int tile = 0; tile < sg.n_tiles; ++tile, ++gt) {
+          for (; qc < 4; ++qc) {
+            mbar_wait(kv_full(gt, qc), kv_phase(gt, qc), abort_flag, err);
+            tc_fence_after();
+            qk_chunk(gt, qc);
+          }
+          mma_commit(bar(kSFull));
+          // until P^T comes: as much of the next tile's first product as has
+          // arrived (two chunks at most: the others' slots are this tile's)
+          qc = 0;
+          const bool more = tile + 1 < sg.n_tiles;
+          while (more && qc < kSlots - 4 && !mbar_test(bar(kPFull), gt & 1u) && !*abort_flag) {
+            if (mbar_test(kv_full(gt + 1, qc), kv_phase(gt + 1, qc))) {
+              tc_fence_after();
+              qk_chunk(gt + 1, qc);
+              ++qc;
+            }
+          }
+          mbar_wait(bar(kPFull), gt & 1u, abort_flag, err);
+          if (tile == 0 && active > 0) mbar_wait(bar(kEpiDone), (active - 1) & 1u, abort_flag, err);
+          tc_fence_after();
+          const uint32_t acc0 = tile == 0 ? 0u : 1u;
+          for (int c = 0; c < 4; ++c) {
+            const uint32_t slot = (4 * gt + c) % kSlots;
+#pragma unroll
+            for (int kk = 0; kk < kKT / 16; ++kk)
+              mma_bf16(tmem + 128u + 64u * c, pv_a0 + ((slot * kSlot + kk * 2048u) >> 4), pv_b0 + ((kk * 2048u) >> 4),
+                       kIdescPV, kk == 0 ? acc0 : 1u);
+            mma_commit(bar(kKVEmpty + slot));
+          }
+          mma_commit(bar(kPVDone));
+        }
+      }
+      __syncwarp();
+      ++active;
+    }
+    if (lane == 0) {
+      // drain: every MMA issued has finished before the block exits
+      mma_commit(bar(kDrain));
+      mbar_wait(bar(kDrain), 0, abort_flag, err);
+    }
+    __syncwarp();
+  } else if (tid < kPtr0) {
+    // =================== gather ===================
+    const int pt = tid - kPG0;  // 0..127
+    uint32_t gt = 0, done = 0, sent = 0;  // chunks announced / issued
+    auto announce = [&](uint32_t u) {
+      fence_async_smem();
+      mbar_arrive(bar(kKVFull + u % kSlots));
+    };
+    // before a wait that may be long: announce the chunks in flight as they land
+    auto settle = [&]() {
+      if (kFp8) return;
+      if (sent - done >= 3) { cp_async_wait<2>(); announce(done++); }
+      if (sent - done >= 2) { cp_async_wait<1>(); announce(done++); }
+      if (sent - done >= 1) { cp_async_wait<0>(); announce(done++); }
+    };
+    auto wait_for = [&](uint32_t b, uint32_t ph) {
+      if (mbar_test(b, ph)) return;
+      settle();
+      mbar_wait(b, ph, abort_flag, err);
+    };
+    auto acquire = [&](uint32_t u) {  // chunk u's slot
+      if (u >= kSlots) wait_for(bar(kKVEmpty + u % kSlots), (u / kSlots - 1) & 1u);
+    };
+    while (next_segment(a, walk, sg)) {
+      for (int tile = 0; tile < sg.n_tiles; ++tile, ++gt) {
+        const uint32_t rs = gt % kAhead;
+        wait_for(bar(kRowFull + rs), (gt / kAhead) & 1u);
+        const unsigned long long* rp = rows + rs * kKT;
+        // (the softmax of the tile before last is over: a slot of it was reused)
+        if (pt < kKT) vflag[(gt & 1u) * kKT + pt] = rp[pt] != 0;
+        if (!kFp8) {
+          const int piece = pt & 15;  // 16-byte piece of a row's 256 bytes
+          for (int c = 0; c < 4; ++c) {
+            const uint32_t u = 4 * gt + c;
+            acquire(u);
+            const uint32_t blk = kv_base + (u % kSlots) * kSlot + (uint32_t)(piece >> 3) * kBlk;
+#pragma unroll
+            for (int i = 0; i < kKT / 8; ++i) {
+              const int row = (pt >> 4) + 8 * i;
+              const uint16_t* src = reinterpret_cast<const uint16_t*>(rp[row]);
+              const uint32_t dst = blk + sw128(row, piece & 7);
+              if (src) cp_async16(dst, src + c * 128 + piece * 8);
+              else st_shared_zero16(dst);
+            }
+            cp_async_commit();
+            ++sent;
+            if (sent - done > 3) {
+              cp_async_wait<3>();
+              announce(done++);
+            }
+          }
+        } else {
+          // FP8 rows: a thread takes 16 dims of six rows; the codes of a chunk
+          // are loaded before its slot is waited for, expanded (code times
+          // the block's power of two, exact in bf16) and stored.  Rows of the
+          // window and the RoPE dims are bf16 and copied as they are.
+          const int p8 = pt & 7;
+          for (int c = 0; c < 4; ++c) {
+            const uint32_t u = 4 * gt + c;
+            const bool codes = c < 3 || p8 < 4;
+            uint4 w0[6], w1[6];
+            uint32_t sc[6];
+#pragma unroll
+            for (int i = 0; i < 6; ++i) {
+              const unsigned long long v = rp[(pt >> 3) + 16 * i];
+              const uint8_t* src = reinterpret_cast<const uint8_t*>(v & ~1ull);
+              w0[i] = w1[i] = make_uint4(0, 0, 0, 0);
+              sc[i] = 0;
+              if (v & 1ull) {
+                if (codes) {
+                  w0[i] = *reinterpret_cast<const uint4*>(src + c * 128 + p8 * 16);
+                  sc[i] = src[kD - a.R + 2 * a.R + 4 * c + (p8 >> 1)];
+                } else {  // dims 448 + 16 (p8 - 4) ..
+                  w0[i] = *reinterpret_cast<const uint4*>(src + 448 + (p8 - 4) * 32);
+                  w1[i] = *reinterpret_cast<const uint4*>(src + 448 + (p8 - 4) * 32 + 16);
+                }
+              } else if (v) {
+                w0[i] = *reinterpret_cast<const uint4*>(src + c * 256 + p8 * 32);
+                w1[i] = *reinterpret_cast<const uint4*>(src + c * 256 + p8 * 32 + 16);
+              }
+            }
+            acquire(u);
+            const uint32_t blk = kv_base + (u % kSlots) * kSlot + (uint32_t)(p8 >> 2) * kBlk;
+            const int q0 = (2 * p8) & 7;  // 16-byte piece of the 128-byte row
+#pragma unroll
+            for (int i = 0; i < 6; ++i) {
+              const int row = (pt >> 3) + 16 * i;
+              if (codes && (rp[row] & 1ull)) {
+                const float s = mx_scale((int)sc[i]);
+                const uint32_t wd[4] = {w0[i].x, w0[i].y, w0[i].z, w0[i].w};
+                uint32_t o[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                  const float2 f = mul_f2(e4m3x2_to_f2(wd[k >> 1] >> (16 * (k & 1))), make_float2(s, s));
+                  o[k] = f2_to_bf2x2(f.x, f.y);
+                }
+                w0[i] = make_uint4(o[0], o[1], o[2], o[3]);
+                w1[i] = make_uint4(o[4], o[5], o[6], o[7]);
+              }
+              st_shared16(blk + sw128(row, q0), w0[i].x, w0[i].y, w0[i].z, w0[i].w);
+              st_shared16(blk + sw128(row, q0 + 1), w1[i].x, w1[i].y, w1[i].z, w1[i].w);
+            }
+            announce(u);
+          }
+        }
+        mbar_arrive(bar(kRowEmpty + rs));
+      }
+    }
+    settle();
+    cp_async_wait<0>();  // nothing of this block is in flight at exit
+  } else {
+    // =================== row addresses ===================
+    const int key = tid - kPtr0;  // 0..95
+    uint32_t gt = 0;
+    while (next_segment(a, walk, sg)) {
+      for (int tile = 0; tile < sg.n_tiles; ++tile, ++gt) {
+        const int j = (sg.tile0 + tile) * kKT + key;
+        bool fp8 = false;
+        const uint8_t* row = j < sg.seq.n_keys ? paged_key(a, sg.b, sg.seq, j, &fp8) : nullptr;
+        if (row) prefetch_l2_bulk(row, fp8 ? (uint32_t)a.row_bytes : kD * 2u);
+        if (gt >= kAhead) mbar_wait(bar(kRowEmpty + gt % kAhead), (gt / kAhead - 1) & 1u, abort_flag, err);
+        rows[(gt % kAhead) * kKT + key] = reinterpret_cast<unsigned long long>(row) | (fp8 ? 1ull : 0ull);
+        mbar_arrive(bar(kRowFull + gt % kAhead));
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
+}
+
+}  // namespace
+
+// FP8 rows: 448 codes in blocks of 32 and 64 RoPE dims, as the gather reads them
+bool paged_tc_supported(const PagedArgs& a, int fmt) {
+  return a.D == kD && (a.R % 2) == 0 && a.R <= 256 && (fmt == 0 || a.R == 64);
+}
+
+void paged_shape_tc(PagedArgs* a) {
+  a->hn = kH;
+  a->kt = kKT;
+  a->G = 148;
+}
+
+cudaError_t launch_paged_attend_tc(const PagedArgs& a, cudaStream_t s) {
+  static std::atomic<int> cache[kMaxDevices], cache8[kMaxDevices];
+  const bool fp8 = a.fmt != 0;
+  const cudaError_t e = fp8 ? ensure_smem(paged_attend_tc_kernel<true>, (int)kSmemBytes, cache8)
+                            : ensure_smem(paged_attend_tc_kernel<false>, (int)kSmemBytes, cache);
+  if (e != cudaSuccess) return e;
+  TraceScope tr("paged_attend_tc", s);
+  return fp8 ? launch_pdl(paged_attend_tc_kernel<true>, dim3(a.G), dim3(kThreads), kSmemBytes, s, a)
+             : launch_pdl(paged_attend_tc_kernel<false>, dim3(a.G), dim3(kThreads), kSmemBytes, s, a);
+}
+
+}  // namespace ds4a
