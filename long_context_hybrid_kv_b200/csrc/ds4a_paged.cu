@@ -41,19 +41,15 @@ __global__ void __launch_bounds__(kGenThreads) paged_attend_generic_kernel(const
   __syncthreads();
   const PagedRange r = s_r;
   const float scale2 = a.scale * kLog2e;
-  int item = r.item, item_t0 = r.item_t0;
-  for (int t = r.t0; t < r.t1;) {
-    const int b = item / a.hgroups, g = item % a.hgroups;
-    const PagedSeq s = paged_seq(a, b);
-    const int n_tiles = paged_tiles(a, s);
-    if (t >= item_t0 + n_tiles) {  // an item without tiles, or the next one
-      item_t0 += n_tiles;
-      ++item;
-      continue;
-    }
-    const int t_end = min(r.t1, item_t0 + n_tiles);
-    const bool whole = t == item_t0 && t_end == item_t0 + n_tiles;
-    const int hb = g * kGenHeads, nh = min(kGenHeads, a.H - hb);
+  if (blockIdx.x == 0 && tid == 0) *a.total = r.total;
+  if (tid == 0) a.cut[blockIdx.x] = make_int4(-1, 0, 0, 0);
+  PagedWalk walk(r);
+  PagedSegment sg;
+  while (paged_next(a, walk, sg)) {
+    const int b = sg.b;
+    const PagedSeq& s = sg.seq;
+    const int hb = sg.g * kGenHeads, nh = min(kGenHeads, a.H - hb);
+    if (tid == 0 && sg.cut_last >= 0) a.cut[blockIdx.x] = make_int4(sg.item, sg.cut_last, sg.slot, 0);
     __syncthreads();
     // q^ = RoPE(RMSNorm(q) g): a warp a head
     if (warp < nh) {
@@ -82,8 +78,10 @@ __global__ void __launch_bounds__(kGenThreads) paged_attend_generic_kernel(const
     float acc[kAcc];
 #pragma unroll
     for (int i = 0; i < kAcc; ++i) acc[i] = 0.f;
-    for (; t < t_end; ++t) {
-      const int j0 = (t - item_t0) * kGenKeys;
+    for (int i = 0; i < sg.n_tiles; ++i) {
+      const int j0 = (sg.tile0 + i) * kGenKeys;
+      const int64_t t = sg.t + i;
+      if (a.weights && tid == 0) a.tile_of[t] = make_int2(sg.item, sg.tile0 + i);
       __syncthreads();
       bool live = false;
       for (int j = warp; j < kGenKeys; j += kGenThreads / 32) {
@@ -122,9 +120,9 @@ __global__ void __launch_bounds__(kGenThreads) paged_attend_generic_kernel(const
         ml[warp] = mn;
         ml[kGenHeads + warp] = ml[kGenHeads + warp] * f + l;
         ml[2 * kGenHeads + warp] = f;
-        if (a.weights) a.tile_ref[(int64_t)t * kGenHeads + warp] = mn;
+        if (a.weights) a.tile_ref[t * kGenHeads + warp] = mn;
       }
-      if (a.weights) a.tile_p[((int64_t)t * kGenKeys + lane) * kGenHeads + warp] = f2bf(p);
+      if (a.weights) a.tile_p[(t * kGenKeys + lane) * kGenHeads + warp] = f2bf(p);
       __syncthreads();
 #pragma unroll
       for (int i = 0; i < kAcc; ++i) {
@@ -137,16 +135,15 @@ __global__ void __launch_bounds__(kGenThreads) paged_attend_generic_kernel(const
       }
     }
     __syncthreads();
-    if (whole) {
+    if (sg.whole) {
       // finished here: the sink joins the denominator, the rope slice turns back
       if (tid < nh) {
         const float mx = ml[tid] / kLog2e;
         const float den = ml[tid] == -INFINITY ? 0.f : ml[kGenHeads + tid] + expf(a.sink[hb + tid] - mx);
         ml[2 * kGenHeads + tid] = den > 0.f ? 1.f / den : 0.f;
-        if (a.weights) {
-          a.whole_ml[(int64_t)item * 2 * kGenHeads + tid] = mx;
-          a.whole_ml[(int64_t)item * 2 * kGenHeads + kGenHeads + tid] = ml[kGenHeads + tid];
-        }
+        if (a.weights)
+          a.lse2[(int64_t)sg.item * kGenHeads + tid] =
+              den > 0.f ? ml[tid] + log2f(den) : a.sink[hb + tid] * kLog2e;
       }
       __syncthreads();
 #pragma unroll
@@ -168,8 +165,7 @@ __global__ void __launch_bounds__(kGenThreads) paged_attend_generic_kernel(const
         *reinterpret_cast<unsigned int*>(a.out + ((int64_t)b * a.H + hb + h) * D + d) = f2_to_bf2x2(x0, x1);
       }
     } else {
-      const int slot = 2 * blockIdx.x + (item == r.item ? 0 : 1);
-      float* part = a.part + (int64_t)slot * (2 * kGenHeads + kGenHeads * D);
+      float* part = paged_part(a, blockIdx.x, sg.slot);
       if (tid < kGenHeads) {
         part[tid] = ml[tid] / kLog2e;  // -inf stays
         part[kGenHeads + tid] = ml[kGenHeads + tid];
@@ -185,118 +181,168 @@ __global__ void __launch_bounds__(kGenThreads) paged_attend_generic_kernel(const
 
 // ---------------------------------------------------------------------------
 // Joining: out = sum_s e^(m_s - M) acc_s / (sum_s e^(m_s - M) l_s + e^(sink -
-// M)) over an item's segments s, then the rope slice turned back.  One block
-// per (head, sequence), a thread a pair of dims.
+// M)) over a cut item's segments s, then the rope slice turned back.  Only
+// cut items are looked at (at most one a block of the attention): every block
+// lists them and takes (item, head) pairs in turn.  Four groups of 64 threads
+// take the segments in turn, a thread eight dims, and are added in order.
+// Bound by L2: an accumulator is read once, half a microsecond or more after
+// it was written.
 // ---------------------------------------------------------------------------
-constexpr int kJoinThreads = 256;
-
-struct JoinItem {
-  int t0, t1, total, c0, c1;  // tiles; blocks that hold segments
-};
-__device__ __forceinline__ JoinItem join_item(const PagedArgs& a, int item) {
-  JoinItem j;
-  j.t0 = a.first[item];
-  j.t1 = a.first[item + 1];
-  j.total = a.first[a.B * a.hgroups];
-  j.c0 = j.c1 = 0;
-  if (j.t1 > j.t0) {
-    j.c0 = paged_block_of(j.t0, j.total, a.G);
-    j.c1 = paged_block_of(j.t1 - 1, j.total, a.G);
-  }
-  return j;
-}
-// segment of block c: in its first slot if the block's tiles begin inside the item
-__device__ __forceinline__ const float* join_part(const PagedArgs& a, const JoinItem& j, int c) {
-  const int slot = 2 * c + (paged_start(c, j.total, a.G) >= j.t0 ? 0 : 1);
-  return a.part + (int64_t)slot * (2 * a.hn + (int64_t)a.hn * a.D);
-}
+constexpr int kJoinThreads = 256, kJoinGroups = 4;
+constexpr int kMaxBlocks = 512;  // of the attention's grid
 
 __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_constant__ PagedArgs a) {
-  const int h = blockIdx.x, b = blockIdx.y, g = h / a.hn, hl = h % a.hn;
+  __shared__ int4 cuts[kMaxBlocks];
+  __shared__ int from[kMaxBlocks];
+  __shared__ float wt[kMaxBlocks];
+  __shared__ int n_cuts;
+  __shared__ float s_l;
+  __shared__ __align__(16) float acc[kJoinGroups][512];
+  const int tid = threadIdx.x, D = a.D;
   pdl_trigger();
   pdl_wait();
-  const int pos = a.q_pos[b];
-  if (pos < 0) return;
-  const JoinItem j = join_item(a, b * a.hgroups + g);
-  const int D = a.D;
-  uint16_t* orow = a.out + ((int64_t)b * a.H + h) * D;
-  if (j.t1 == j.t0) {  // no keys at all: nothing but the sink
-    for (int d = 2 * threadIdx.x; d < D; d += 2 * kJoinThreads) *reinterpret_cast<unsigned int*>(orow + d) = 0u;
-    return;
-  }
-  if (j.c0 == j.c1) return;  // finished by its block
-  float M = -INFINITY;
-  for (int c = j.c0; c <= j.c1; ++c) M = fmaxf(M, join_part(a, j, c)[hl]);
-  for (int d = 2 * threadIdx.x; d < D; d += 2 * kJoinThreads) {
-    float L = 0.f, x0 = 0.f, x1 = 0.f;
-    if (M != -INFINITY) {
-      for (int c = j.c0; c <= j.c1; ++c) {
-        const float* p = join_part(a, j, c);
-        const float e = __expf(p[hl] - M);  // 0 for a segment without keys
-        if (e == 0.f) continue;
-        const float2 v = *reinterpret_cast<const float2*>(p + 2 * a.hn + (int64_t)hl * D + d);
-        L = fmaf(p[a.hn + hl], e, L);
-        x0 = fmaf(v.x, e, x0);
-        x1 = fmaf(v.y, e, x1);
+  if (tid < 32) {
+    int n = 0;
+    for (int c0 = 0; c0 < a.G; c0 += 32) {
+      const int c = c0 + tid;
+      const int4 v = c < a.G ? a.cut[c] : make_int4(-1, 0, 0, 0);
+      const unsigned int m = __ballot_sync(0xffffffffu, v.x >= 0);
+      if (v.x >= 0) {
+        const int at = n + __popc(m & ((1u << tid) - 1u));
+        cuts[at] = v;
+        from[at] = c;
       }
-      const float inv = 1.f / (L + __expf(a.sink[h] - M));
-      x0 *= inv;
-      x1 *= inv;
+      n += __popc(m);
     }
-    if (d >= D - a.R) {
-      float c, sn;
-      rope_cos_sin(pos, a.rope.t[(d - (D - a.R)) >> 1], &c, &sn);
-      const float y0 = x0 * c + x1 * sn;
-      x1 = -x0 * sn + x1 * c;
-      x0 = y0;
+    if (tid == 0) n_cuts = n;
+  }
+  if (a.W == 0)  // sequences without any key: nothing but the sink
+    for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
+      const PagedSeq s = paged_seq(a, b);
+      if (s.pos >= 0 && s.n_keys == 0)
+        for (int e = tid; e < a.H * D / 2; e += kJoinThreads)
+          reinterpret_cast<unsigned int*>(a.out + (int64_t)b * a.H * D)[e] = 0u;
     }
-    *reinterpret_cast<unsigned int*>(orow + d) = f2_to_bf2x2(x0, x1);
+  __syncthreads();
+  const int grp = tid >> 6, l64 = tid & 63;
+  for (int u = blockIdx.x; u < n_cuts * a.hn; u += gridDim.x) {
+    const int4 cut = cuts[u / a.hn];
+    const int c0 = from[u / a.hn], hl = u % a.hn, n_seg = cut.y - c0 + 1;
+    const int b = cut.x / a.hgroups, h = (cut.x - b * a.hgroups) * a.hn + hl;
+    if (h >= a.H) continue;
+    auto part_of = [&](int s) { return paged_part(a, c0 + s, s == 0 ? cut.z : 0); };
+    __syncthreads();
+    if (tid < 32) {
+      float M = -INFINITY, L = 0.f;
+      for (int s = tid; s < n_seg; s += 32) {
+        wt[s] = part_of(s)[hl];
+        M = fmaxf(M, wt[s]);
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+      for (int s = tid; s < n_seg; s += 32) {
+        const float e = M == -INFINITY ? 0.f : __expf(wt[s] - M);
+        wt[s] = e;
+        L = fmaf(part_of(s)[a.hn + hl], e, L);
+      }
+      L = warp_sum(L);
+      if (tid == 0) {
+        const float sk = a.sink[h], top = fmaxf(M, sk);
+        s_l = M == -INFINITY ? 0.f : 1.f / (L + __expf(sk - M));
+        if (a.weights) a.lse2[(int64_t)cut.x * a.hn + hl] = (top + logf(L * expf(M - top) + expf(sk - top))) * kLog2e;
+      }
+    }
+    __syncthreads();
+    const float inv = s_l;
+    const int pos = a.q_pos[b];
+    for (int d0 = 0; d0 < D; d0 += 512) {
+      const int d = d0 + 8 * l64;
+      if (d < D) {
+        float x[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = 0.f;
+#pragma unroll 4
+        for (int s = grp; s < n_seg; s += kJoinGroups) {
+          const float4* p = reinterpret_cast<const float4*>(part_of(s) + 2 * a.hn + (int64_t)hl * D + d);
+          const float4 v = p[0], w = p[1];
+          const float e = wt[s];
+          if (e != 0.f) {  // (a segment without a key that counts may hold anything)
+            x[0] = fmaf(v.x, e, x[0]); x[1] = fmaf(v.y, e, x[1]); x[2] = fmaf(v.z, e, x[2]); x[3] = fmaf(v.w, e, x[3]);
+            x[4] = fmaf(w.x, e, x[4]); x[5] = fmaf(w.y, e, x[5]); x[6] = fmaf(w.z, e, x[6]); x[7] = fmaf(w.w, e, x[7]);
+          }
+        }
+        *reinterpret_cast<float4*>(&acc[grp][8 * l64]) = make_float4(x[0], x[1], x[2], x[3]);
+        *reinterpret_cast<float4*>(&acc[grp][8 * l64 + 4]) = make_float4(x[4], x[5], x[6], x[7]);
+      }
+      __syncthreads();
+      const int e = 2 * tid, dd = d0 + e;
+      if (e < 512 && dd < D) {
+        float x0 = 0.f, x1 = 0.f;
+#pragma unroll
+        for (int g = 0; g < kJoinGroups; ++g) {
+          x0 += acc[g][e];
+          x1 += acc[g][e + 1];
+        }
+        x0 *= inv;
+        x1 *= inv;
+        if (dd >= D - a.R) {
+          float cs, sn;
+          rope_cos_sin(pos, a.rope.t[(dd - (D - a.R)) >> 1], &cs, &sn);
+          const float y0 = x0 * cs + x1 * sn;
+          x1 = -x0 * sn + x1 * cs;
+          x0 = y0;
+        }
+        *reinterpret_cast<unsigned int*>(a.out + ((int64_t)b * a.H + h) * D + dd) = f2_to_bf2x2(x0, x1);
+      }
+    }
   }
 }
 
-// Attention weight of a slot: sum over the heads of p e^(ref - lse), from the
-// probabilities that the attention left per tile.  A warp a key.
+// Attention weight of a slot: sum over the heads of p 2^(ref - lse2), from
+// the probabilities that the attention left per tile (128 bytes a key for 64
+// heads).  A block a tile; the factors 2^(ref - lse2) once a tile, four
+// threads a key.
 __global__ void __launch_bounds__(kJoinThreads) paged_weights_kernel(const __grid_constant__ PagedArgs a) {
-  __shared__ float lse2[128];
-  const int b = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  __shared__ float f[128];
+  const int tid = threadIdx.x, hn = a.hn;
   pdl_trigger();
   pdl_wait();
-  const int pos = a.q_pos[b];
-  const int n = paged_entries(a, b, pos);
-  if (n > a.w_len && blockIdx.x == 0 && tid == 0) raise_err(a.err, DS4A_DEV_BAD_INDEX);
-  const int n_w = min(n, a.w_len);
-  if ((int)blockIdx.x * a.kt >= n_w) return;
-  for (int h = tid; h < a.H; h += kJoinThreads) {
-    const int item = b * a.hgroups + h / a.hn, hl = h % a.hn;
-    const JoinItem j = join_item(a, item);
-    float M = -INFINITY, L = 0.f;
-    if (j.c0 == j.c1) {
-      M = a.whole_ml[(int64_t)item * 2 * a.hn + hl];
-      L = a.whole_ml[(int64_t)item * 2 * a.hn + a.hn + hl];
-    } else {
-      for (int c = j.c0; c <= j.c1; ++c) M = fmaxf(M, join_part(a, j, c)[hl]);
-      for (int c = j.c0; c <= j.c1; ++c) {
-        const float* p = join_part(a, j, c);
-        if (p[hl] != -INFINITY) L = fmaf(p[a.hn + hl], expf(p[hl] - M), L);
-      }
+  const int total = *a.total;
+  for (int t = blockIdx.x; t < total; t += gridDim.x) {
+    const int2 at = a.tile_of[t];
+    const int b = at.x / a.hgroups;
+    if (at.x != b * a.hgroups) continue;  // the sequence's first group sums them all
+    const PagedSeq s = paged_seq(a, b);
+    const int n_tiles = paged_tiles(a, s), j0 = at.y * a.kt;
+    if (at.y == 0 && tid == 0 && s.n > a.w_len) raise_err(a.err, DS4A_DEV_BAD_INDEX);
+    __syncthreads();
+    for (int h = tid; h < a.H; h += kJoinThreads) {
+      const int g = h / hn;
+      f[h] = exp2f(a.tile_ref[((int64_t)t + (int64_t)g * n_tiles) * hn + h % hn] - a.lse2[(int64_t)(at.x + g) * hn + h % hn]);
     }
-    // log of the denominator, sink included, in log2 units
-    const float sk = a.sink[h], top = fmaxf(M, sk);
-    lse2[h] = (top + logf(L * expf(M - top) + expf(sk - top))) * kLog2e;
-  }
-  __syncthreads();
-  for (int s0 = blockIdx.x * a.kt; s0 < n_w; s0 += gridDim.x * a.kt) {
-    const int tile = s0 / a.kt;
-    for (int i = warp; i < a.kt && s0 + i < n_w; i += kJoinThreads / 32) {
+    __syncthreads();
+    for (int i0 = 0; i0 < a.kt; i0 += kJoinThreads / 4) {
+      const int i = i0 + (tid >> 2), q = tid & 3;
       float w = 0.f;
-      for (int h = lane; h < a.H; h += 32) {
-        const int64_t t = a.first[b * a.hgroups + h / a.hn] + tile;
-        const float p = bf2f(a.tile_p[(t * a.kt + i) * a.hn + h % a.hn]);
-        const float ref = a.tile_ref[t * a.hn + h % a.hn];
-        if (p > 0.f) w += p * exp2f(ref - lse2[h]);
-      }
-      w = warp_sum(w);
-      if (lane == 0) a.weights[(int64_t)b * a.w_stride + s0 + i] = f2bf(w);
+      if (i < a.kt)
+        for (int g = 0; g < a.hgroups; ++g) {
+          const uint16_t* p = a.tile_p + (((int64_t)t + (int64_t)g * n_tiles) * a.kt + i) * hn;
+          for (int c = 8 * q; c < hn; c += 32) {
+            const uint4 v = *reinterpret_cast<const uint4*>(p + c);
+            const unsigned int x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float2 y = bf2x2_to_f2(x[k]);
+              const int h = g * hn + c + 2 * k;
+              if (h < a.H) w = fmaf(y.x, f[h], w);
+              if (h + 1 < a.H) w = fmaf(y.y, f[h + 1], w);
+            }
+          }
+        }
+      w += __shfl_xor_sync(0xffffffffu, w, 1);
+      w += __shfl_xor_sync(0xffffffffu, w, 2);
+      const int j = j0 + i;
+      if (q == 0 && i < a.kt && j < s.n && j < a.w_len) a.weights[(int64_t)b * a.w_stride + j] = f2bf(w);
     }
   }
 }
@@ -312,15 +358,15 @@ cudaError_t launch_paged_attend_generic(const PagedArgs& a, cudaStream_t s) {
   return launch_pdl(paged_attend_generic_kernel, dim3(a.G), dim3(kGenThreads), smem, s, a);
 }
 
-cudaError_t launch_paged_join(const PagedArgs& a, cudaStream_t s) {
-  {
+cudaError_t launch_paged_join(const PagedArgs& a, int tiles, cudaStream_t s) {
+  if (a.G > 1 || a.W == 0) {  // (one block cuts nothing)
     TraceScope tr("paged_join", s);
-    const cudaError_t e = launch_pdl(paged_join_kernel, dim3(a.H, a.B), dim3(kJoinThreads), 0, s, a);
-    if (e != cudaSuccess || !a.weights) return e;
+    const cudaError_t e = launch_pdl(paged_join_kernel, dim3(min(148 * 6, a.G * a.hn)), dim3(kJoinThreads), 0, s, a);
+    if (e != cudaSuccess) return e;
   }
+  if (!a.weights) return cudaSuccess;
   TraceScope tr("paged_weights", s);
-  const int tiles = (a.cap + a.kt - 1) / a.kt;
-  return launch_pdl(paged_weights_kernel, dim3(min(tiles, max(1, 148 * 8 / a.B)), a.B), dim3(kJoinThreads), 0, s, a);
+  return launch_pdl(paged_weights_kernel, dim3(min(tiles, 148 * 6)), dim3(kJoinThreads), 0, s, a);
 }
 
 void paged_shape_generic(PagedArgs* a) {

@@ -2,27 +2,27 @@
 // rows of 512: "DeepSeek-v4 Beyond Basics" 3.2.2 eq. 19 and 3.3 eqs. 24-27 for
 // one new token per sequence; schedule in ds4a_paged.cuh.
 //
-// All heads read the same rows, so a tile of 96 keys is two dense products with
+// All heads read the same rows, so a tile of 64 keys is two dense products with
 // the keys, then the dims, on the MMA's M side and 64 heads on N:
 //   S^T[key][h]  = KV[key][:] . q^[h][:]      K = 512, A K-major, M = 128
-//   O^T[d][h]   += KV[key][d]^T . P^T[key][h]  K = 96 keys, A MN-major
-// M = 128 reads 32 rows past the tile's 96 (whatever lies behind them in
-// shared memory); an A row only reaches its own row of S^T, and those are not
-// looked at.  96 keys instead of 128 leave room for one and a half tiles next
-// to the 64 KiB of q^: the next tile's rows arrive, and half of its first
-// product runs, during this tile's softmax.  By 44 GB/s of HBM an SM a tile
-// takes 2.2 us, its products 1.4 us (N = 64 is bound by the 6 KiB of shared
-// memory an MMA reads), so that the loads are to be kept going.
+//   O^T[d][h]   += KV[key][d]^T . P^T[key][h]  K = 64 keys, A MN-major
+// M = 128 reads 64 rows past the tile's (whatever lies behind them in shared
+// memory); an A row only reaches its own row of S^T, and those are not looked
+// at.  An MMA of N = 64 is bound by the 6 KiB of shared memory that it reads,
+// so the tile's products take 1.2 us; at 44 GB/s of HBM an SM its rows take
+// 1.5 us.  64 keys, not 128, leave room for nine 128-dim chunks of rows (2.25
+// tiles) next to the 64 KiB of q^, so that the next tile is there and its
+// first product runs during this tile's softmax.
 //
-// Thread block (one per SM, 512 threads):
+// Thread block (one per SM, 480 threads):
 //   warps 0-7    q^ of every segment, softmax, epilogue: two warps per TMEM
-//                lane quarter with 32 heads each; thread = key row of S^T,
-//                later dim row of O^T (the last quarter holds no keys).
+//                lane quarter with 32 heads each; thread = key row of S^T
+//                (the upper two quarters hold none), later dim row of O^T.
 //   warp 8       TMEM allocation; lane 0 issues the MMAs.
-//   warps 9-12   gather the rows by cp.async, 128 dims (24 KiB) at a time,
-//                into a ring of six such slots, in the 128-byte swizzle.  FP8
-//                rows go through registers and are expanded on the way.
-//   warps 13-15  one key a thread, up to four tiles ahead: index, page, row
+//   warps 9-12   gather the rows by cp.async, a chunk (16 KiB) at a time, into
+//                a ring of nine, in the 128-byte swizzle.  FP8 rows go through
+//                registers and are expanded on the way.
+//   warps 13-14  one key a thread, up to four tiles ahead: index, page, row
 //                address, and a prefetch of the row into L2, so that HBM keeps
 //                streaming while the ring is full.
 #include "ds4a_paged.cuh"
@@ -34,12 +34,12 @@ namespace {
 using namespace tc;
 
 constexpr int kH = 64, kD = 512;
-constexpr int kKT = 96;               // keys per tile
-constexpr int kThreads = 512;
+constexpr int kKT = 64;               // keys per tile
+constexpr int kThreads = 480;
 constexpr int kMmaWarp = 8;
 constexpr int kPG0 = 288;             // first gathering thread (warps 9-12)
-constexpr int kPtr0 = 416;            // first address thread (warps 13-15)
-constexpr int kSlots = 6;             // ring of 128-dim chunks
+constexpr int kPtr0 = 416;            // first address thread (warps 13-14)
+constexpr int kSlots = 9;             // ring of 128-dim chunks
 constexpr int kAhead = 4;             // tiles of row addresses
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kRescaleLog2 = 8.0f;  // O^T is rescaled when a head's maximum grows by more than 2^8
@@ -49,17 +49,17 @@ constexpr uint32_t kBlk = kKT * 128;   // 64 dims of a tile's keys
 constexpr uint32_t kSlot = 2 * kBlk;   // 128 dims
 constexpr uint32_t kOffKV = 0;
 constexpr uint32_t kOffQ = kSlots * kSlot;       // 8 blocks x [64 heads][128 B]
-constexpr uint32_t kOffP = kOffQ + 65536;        // [96 keys][128 B]
+constexpr uint32_t kOffP = kOffQ + 65536;        // [64 keys][128 B]
 constexpr uint32_t kOffBar = kOffP + kBlk;
-constexpr uint32_t kOffMisc = kOffBar + 256;     // abort flag, TMEM address, the block's range
-constexpr uint32_t kOffRow = kOffMisc + 64;      // [4 tiles][96] row addresses, bit 0: FP8
+constexpr uint32_t kOffMisc = kOffBar + 320;     // abort flag, TMEM address, the block's range
+constexpr uint32_t kOffRow = kOffMisc + 64;      // [4 tiles][64] row addresses, bit 0: FP8
 constexpr uint32_t kOffRed = kOffRow + kAhead * kKT * 8;  // [4][64] floats
 constexpr uint32_t kOffMrun = kOffRed + 1024;
 constexpr uint32_t kOffAlpha = kOffMrun + 256;
 constexpr uint32_t kOffInv = kOffAlpha + 256;
 constexpr uint32_t kOffSink = kOffInv + 256;
-constexpr uint32_t kOffValid = kOffSink + 256;   // [2 tiles][96]
-constexpr uint32_t kSmemBytes = kOffValid + 2 * kKT + 1024;
+constexpr uint32_t kOffRope = kOffSink + 256;    // [128] (cos, sin) of the segment's position
+constexpr uint32_t kSmemBytes = kOffRope + 1024 + 1024;
 static_assert(kSmemBytes <= 232448, "shared memory of a block");
 // The finished output goes out through the q^ and P^T buffers, a head's 1024
 // bytes 1088 apart (the two heads that a warp writes at a time then lie in
@@ -69,9 +69,9 @@ static_assert(kH * kStagePitch <= 65536 + kBlk, "output stage");
 
 enum Bar {
   kKVFull = 0, kKVEmpty = kKVFull + kSlots, kRowFull = kKVEmpty + kSlots, kRowEmpty = kRowFull + kAhead,
-  kQFull = kRowEmpty + kAhead, kSFull, kPFull, kPVDone, kEpiDone, kDrain, kNumBars
+  kQFull = kRowEmpty + kAhead, kSFull0, kSFull1, kPFull, kPVDone, kEpiDone, kDrain, kNumBars
 };
-static_assert(kNumBars * 8 <= 256, "barriers");
+static_assert(kNumBars * 8 <= 320, "barriers");
 
 constexpr uint32_t kIdescQK = idesc_bf16(128, 64, 0, 0);
 constexpr uint32_t kIdescPV = idesc_bf16(128, 64, 1, 1);
@@ -79,44 +79,6 @@ constexpr uint32_t kIdescPV = idesc_bf16(128, 64, 1, 1);
 // smem -> global, 16-byte aligned, in the thread's bulk group
 __device__ __forceinline__ void bulk_s2g(void* dst, uint32_t src, uint32_t bytes) {
   asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src), "r"(bytes) : "memory");
-}
-
-// The segments of a block one after the other (every role walks them alike).
-struct Walk {
-  int t, t1, item, item_t0, first_item;
-  __device__ __forceinline__ Walk(const PagedRange& r)
-      : t(r.t0), t1(r.t1), item(r.item), item_t0(r.item_t0), first_item(r.item) {}
-};
-struct Segment {
-  int item, b, g, tile0, n_tiles, slot;  // tiles counted in the item; slot of a partial result
-  int t;                                 // first tile in the row of all tiles
-  bool whole;
-  PagedSeq seq;
-};
-__device__ __forceinline__ bool next_segment(const PagedArgs& a, Walk& w, Segment& s) {
-  while (w.t < w.t1) {
-    s.item = w.item;
-    s.b = w.item / a.hgroups;
-    s.g = w.item - s.b * a.hgroups;
-    s.seq = paged_seq(a, s.b);
-    const int n = paged_tiles(a, s.seq), end = w.item_t0 + n;
-    if (w.t >= end) {  // no tiles
-      w.item_t0 = end;
-      ++w.item;
-      continue;
-    }
-    const int stop = min(w.t1, end);
-    s.t = w.t;
-    s.tile0 = w.t - w.item_t0;
-    s.n_tiles = stop - w.t;
-    s.whole = s.n_tiles == n;
-    s.slot = 2 * blockIdx.x + (w.item == w.first_item ? 0 : 1);
-    w.t = stop;
-    w.item_t0 = end;
-    ++w.item;
-    return true;
-  }
-  return false;
 }
 
 __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
@@ -127,6 +89,17 @@ __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
       : "r"(bar), "r"(parity)
       : "memory");
   return ok != 0;
+}
+
+// Arrive on the mbarrier when this thread's cp.async so far have landed.  (The
+// rows are written in the generic proxy: the MMA's thread fences the proxies
+// after it has waited for the barrier.)
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+// 16 bytes of zeros by the same path
+__device__ __forceinline__ void cp_async_zero16(uint32_t dst, const void* any) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, 0;" ::"r"(dst), "l"(any) : "memory");
 }
 
 template <bool kFp8>
@@ -146,7 +119,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
   float* alpha_s = reinterpret_cast<float*>(smem + kOffAlpha);
   float* inv_s = reinterpret_cast<float*>(smem + kOffInv);
   float* sink_s = reinterpret_cast<float*>(smem + kOffSink);
-  uint8_t* vflag = smem + kOffValid;
+  float2* rope_s = reinterpret_cast<float2*>(smem + kOffRope);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   unsigned int* err = a.err;
@@ -160,10 +133,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
     }
     for (int i = 0; i < kAhead; ++i) {
       mbar_init(bar(kRowFull + i), kKT);
-      mbar_init(bar(kRowEmpty + i), 128);
+      mbar_init(bar(kRowEmpty + i), 128 + kKT);  // the gatherers and half of the softmax's key threads
     }
     mbar_init(bar(kQFull), 256);
-    mbar_init(bar(kSFull), 1);
+    mbar_init(bar(kSFull0), 1);
+    mbar_init(bar(kSFull1), 1);
     mbar_init(bar(kPFull), 256);
     mbar_init(bar(kPVDone), 1);
     mbar_init(bar(kEpiDone), 256);
@@ -177,123 +151,114 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
   pdl_wait();
   if (warp == 0) {
     const PagedRange r = paged_range(a, blockIdx.x);
-    if (lane == 0) *s_range = r;
+    if (lane == 0) {
+      *s_range = r;
+      if (blockIdx.x == 0) *a.total = r.total;
+    }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  Walk walk(*s_range);
-  Segment sg;
+  PagedWalk walk(*s_range);
+  PagedSegment sg;
 
   if (warp < 8) {
     // =================== q^, softmax, epilogue ===================
     const int q4 = warp & 3, hf = warp >> 2;
     const int r = 32 * q4 + lane;  // key row of S^T / dim row of O^T within a chunk
-    const bool has_key = q4 < 3;
+    const bool has_key = q4 < 2;
     const int st = tid;            // 0..255
     const int h0 = 32 * hf;
     const uint32_t t_lane = tmem + ((uint32_t)(32 * q4) << 16);
     const float scale2 = a.scale * kLog2e;
     const int R = a.R;
-    const float4 g0 = *reinterpret_cast<const float4*>(a.q_norm_g + 8 * lane);
-    const float4 g1 = *reinterpret_cast<const float4*>(a.q_norm_g + 8 * lane + 4);
-    const float4 g2 = *reinterpret_cast<const float4*>(a.q_norm_g + 256 + 8 * lane);
-    const float4 g3 = *reinterpret_cast<const float4*>(a.q_norm_g + 256 + 8 * lane + 4);
     uint32_t gt = 0;
-    while (next_segment(a, walk, sg)) {
+    int4 cut = make_int4(-1, 0, 0, 0);
+    while (paged_next(a, walk, sg)) {
       const int nh = min(kH, a.H - sg.g * kH);
       const int64_t head0 = (int64_t)sg.b * a.H + sg.g * kH;
+      if (sg.cut_last >= 0) cut = make_int4(sg.item, sg.cut_last, sg.slot, 0);
+      // q^ = RoPE_pos(RMSNorm(q) g), rounded to bf16 (the MMA's operand), into
+      // the K-major operand layout: warp w takes heads w, w + 8, ..., lane l
+      // dims 8l .. 8l+7 and 256+8l ..; heads that the group does not have are
+      // 0.  All loads go out first.
+      uint4 va[8], vb[8];
+      {
+        const uint16_t* qrow = a.q + head0 * kD + 8 * lane;
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          const int h = warp + 8 * u;
+          va[u] = vb[u] = make_uint4(0, 0, 0, 0);
+          if (h < nh) {
+            va[u] = *reinterpret_cast<const uint4*>(qrow + h * kD);
+            vb[u] = *reinterpret_cast<const uint4*>(qrow + h * kD + 256);
+          }
+        }
+      }
+      if (st < R / 2) {
+        float cs, sn;
+        rope_cos_sin(sg.seq.pos, a.rope.t[st], &cs, &sn);
+        rope_s[st] = make_float2(cs, sn);
+      }
       if (st < kH) {
         sink_s[st] = st < nh ? a.sink[sg.g * kH + st] * kLog2e : 0.f;
         mrun[st] = kNoRef;
       }
-      // q^ = RoPE_pos(RMSNorm(q) g), rounded to bf16 (the MMA's operand), into
-      // the K-major operand layout: warp w takes heads w, w + 8, ..., lane l
-      // dims 8l .. 8l+7 and 256+8l ..; heads that the group does not have are 0
+      named_bar(1, 256);
       {
-        const uint16_t* qrow = a.q + head0 * kD;
-        float rc[4], rs[4];
+        float2 g[8], rope[4];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          rc[u] = 1.f;
-          rs[u] = 0.f;
-          const int d = 256 + 8 * lane + 2 * u;
-          if (d >= kD - R) rope_cos_sin(sg.seq.pos, a.rope.t[(d - (kD - R)) >> 1], &rc[u], &rs[u]);
+        for (int k = 0; k < 4; ++k) {
+          g[k] = *reinterpret_cast<const float2*>(a.q_norm_g + 8 * lane + 2 * k);
+          g[4 + k] = *reinterpret_cast<const float2*>(a.q_norm_g + 256 + 8 * lane + 2 * k);
+          const int d = 256 + 8 * lane + 2 * k - (kD - R);
+          rope[k] = d >= 0 ? rope_s[d >> 1] : make_float2(1.f, 0.f);
         }
-        const float g[16] = {g0.x, g0.y, g0.z, g0.w, g1.x, g1.y, g1.z, g1.w,
-                             g2.x, g2.y, g2.z, g2.w, g3.x, g3.y, g3.z, g3.w};
         const uint32_t offA = (uint32_t)(lane >> 3) * 8192u, offB = (uint32_t)(4 + (lane >> 3)) * 8192u;
-#pragma unroll 1
-        for (int h4 = warp; h4 < kH; h4 += 32) {
-          uint4 va[4], vb[4];
 #pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            const int h = h4 + 8 * u;
-            va[u] = vb[u] = make_uint4(0, 0, 0, 0);
-            if (h < nh) {
-              va[u] = *reinterpret_cast<const uint4*>(qrow + h * kD + 8 * lane);
-              vb[u] = *reinterpret_cast<const uint4*>(qrow + h * kD + 256 + 8 * lane);
-            }
+        for (int u = 0; u < 8; ++u) {
+          const int h = warp + 8 * u;
+          const unsigned int wv[8] = {va[u].x, va[u].y, va[u].z, va[u].w, vb[u].x, vb[u].y, vb[u].z, vb[u].w};
+          float2 acc = make_float2(0.f, 0.f);
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            const float2 f = bf2x2_to_f2(wv[q]);
+            acc = fma_f2(f, f, acc);
           }
-          float ss[4];
+          // (a head that is not there: 0 rather than 0 / sqrt(eps))
+          const float ss = warp_sum(acc.x + acc.y);
+          const float rstd = h < nh ? rsqrtf(ss * (1.f / kD) + a.eps) : 0.f;
+          uint32_t pq[8];
 #pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            const unsigned int wv[8] = {va[u].x, va[u].y, va[u].z, va[u].w, vb[u].x, vb[u].y, vb[u].z, vb[u].w};
-            float acc = 0.f;
-#pragma unroll
-            for (int q = 0; q < 8; ++q) {
-              const float2 f = bf2x2_to_f2(wv[q]);
-              acc = fmaf(f.x, f.x, fmaf(f.y, f.y, acc));
+          for (int q = 0; q < 8; ++q) {
+            float2 x = mul_f2(mul_f2(bf2x2_to_f2(wv[q]), make_float2(rstd, rstd)), g[q]);
+            if (q >= 4) {
+              const float2 cs = rope[q - 4];
+              x = fma_f2(make_float2(x.x, x.x), cs, mul_f2(make_float2(x.y, x.y), make_float2(-cs.y, cs.x)));
             }
-            ss[u] = acc;
+            pq[q] = f2_to_bf2x2(x.x, x.y);
           }
-#pragma unroll
-          for (int o = 16; o > 0; o >>= 1)
-#pragma unroll
-            for (int u = 0; u < 4; ++u) ss[u] += __shfl_xor_sync(0xffffffffu, ss[u], o);
-#pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            const int h = h4 + 8 * u;
-            // (a head that is not there: 0 rather than 0 * 1/sqrt(eps))
-            const float rstd = h < nh ? rsqrtf(ss[u] / (float)kD + a.eps) : 0.f;
-            const unsigned int wv[8] = {va[u].x, va[u].y, va[u].z, va[u].w, vb[u].x, vb[u].y, vb[u].z, vb[u].w};
-            uint32_t pq[8];
-#pragma unroll
-            for (int q = 0; q < 8; ++q) {
-              const float2 f = bf2x2_to_f2(wv[q]);
-              float x0 = f.x * rstd * g[2 * q], x1 = f.y * rstd * g[2 * q + 1];
-              if (q >= 4) {
-                const float y0 = x0 * rc[q - 4] - x1 * rs[q - 4], y1 = x0 * rs[q - 4] + x1 * rc[q - 4];
-                x0 = y0;
-                x1 = y1;
-              }
-              pq[q] = f2_to_bf2x2(x0, x1);
-            }
-            const uint32_t sw = sw128((uint32_t)h, (uint32_t)(lane & 7));
-            st_shared16(q_base + offA + sw, pq[0], pq[1], pq[2], pq[3]);
-            st_shared16(q_base + offB + sw, pq[4], pq[5], pq[6], pq[7]);
-          }
+          const uint32_t sw = sw128((uint32_t)h, (uint32_t)(lane & 7));
+          st_shared16(q_base + offA + sw, pq[0], pq[1], pq[2], pq[3]);
+          st_shared16(q_base + offB + sw, pq[4], pq[5], pq[6], pq[7]);
         }
-        fence_async_smem();
-        mbar_arrive(bar(kQFull));
       }
+      fence_async_smem();
+      mbar_arrive(bar(kQFull));
       float lpart[32];
 #pragma unroll
       for (int i = 0; i < 32; ++i) lpart[i] = 0.f;
-      named_bar(1, 256);
       for (int tile = 0; tile < sg.n_tiles; ++tile, ++gt) {
-        mbar_wait(bar(kSFull), gt & 1u, abort_flag, err);
-        // the last chunk's barrier (complete before S^T is) orders the
-        // gatherers' flags of this tile before the read
-        mbar_wait(bar(kKVFull + (4 * gt + 3) % kSlots), ((4 * gt + 3) / kSlots) & 1u, abort_flag, err);
+        mbar_wait(bar(kSFull0 + (gt & 1u)), (gt >> 1) & 1u, abort_flag, err);
+        mbar_wait(bar(kRowFull + gt % kAhead), (gt / kAhead) & 1u, abort_flag, err);  // (the tile's addresses)
         tc_fence_after();
         float z[32];
         float lead = -INFINITY;
         if (has_key) {
           // a key slot without a row (zero-filled, so its S^T row is 0) gets
           // -inf through the bias of the scaling FMA
-          const float zbias = vflag[(gt & 1u) * kKT + r] != 0 ? 0.f : -INFINITY;
+          const float zbias = rows[(gt % kAhead) * kKT + r] != 0 ? 0.f : -INFINITY;
           tmem_ld32(t_lane + (gt & 1u) * 64u + (uint32_t)h0, z);
           tmem_ld_wait();
           const float4* mrun4 = reinterpret_cast<const float4*>(mrun + h0);
@@ -312,11 +277,12 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
           }
         }
         const bool rescale = bar_or(1, 256, lead > kRescaleLog2);
+        if (has_key && hf == 0) mbar_arrive(bar(kRowEmpty + gt % kAhead));  // every key thread has read its address
         if (rescale) {
           if (has_key) red[q4 * 64 + h0 + lane] = warp_reduce32<true>(z);
           named_bar(1, 256);
           if (st < kH) {
-            const float mt = fmaxf(fmaxf(red[st], red[64 + st]), red[128 + st]);
+            const float mt = fmaxf(red[st], red[64 + st]);
             const float mo = mrun[st];
             float al = 1.f;
             if (mt > mo + kRescaleLog2) {  // a -inf tile maximum never moves it
@@ -336,7 +302,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
             lpart[4 * i4 + 3] *= a4.w;
           }
         }
-        if (a.weights && st < kH) a.tile_ref[(int64_t)(sg.t + tile) * kH + st] = mrun[st];
+        if (a.weights) {
+          if (st < kH) a.tile_ref[(int64_t)(sg.t + tile) * kH + st] = mrun[st];
+          if (st == 0) a.tile_of[sg.t + tile] = make_int2(sg.item, sg.tile0 + tile);
+        }
         uint32_t pk[16];
         if (has_key) {
 #pragma unroll
@@ -397,20 +366,15 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
       tc_fence_after();
       if (has_key) red[q4 * 64 + h0 + lane] = warp_reduce32<false>(lpart);
       named_bar(1, 256);
-      float* part = a.part + (int64_t)sg.slot * (2 * kH + kH * kD);
+      float* part = paged_part(a, blockIdx.x, sg.slot);
       if (st < kH) {
-        const float l = red[st] + red[64 + st] + red[128 + st];
-        const float m = mrun[st];
-        const float mx = m <= kNoRef ? -INFINITY : m * 0.6931471805599453f;  // natural-log units
+        const float l = red[st] + red[64 + st], m = mrun[st];
         if (sg.whole) {
           const float den = m <= kNoRef ? 0.f : l + exp2f(sink_s[st] - m);
           inv_s[st] = den > 0.f ? 1.f / den : 0.f;
-          if (a.weights) {
-            a.whole_ml[(int64_t)sg.item * 2 * kH + st] = mx;
-            a.whole_ml[(int64_t)sg.item * 2 * kH + kH + st] = l;
-          }
+          if (a.weights) a.lse2[(int64_t)sg.item * kH + st] = den > 0.f ? m + log2f(den) : sink_s[st];
         } else {
-          part[st] = mx;
+          part[st] = m <= kNoRef ? -INFINITY : m * 0.6931471805599453f;  // natural-log units
           part[kH + st] = l;
         }
       }
@@ -429,7 +393,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
           // slice, by -pos) and writes one 4-byte word of the stage
           const bool rot = d >= kD - R;
           float cs = 1.f, sn = 0.f;
-          if (rot) rope_cos_sin(sg.seq.pos, a.rope.t[(d - (kD - R)) >> 1], &cs, &sn);
+          if (rot) {
+            cs = rope_s[(d - (kD - R)) >> 1].x;
+            sn = rope_s[(d - (kD - R)) >> 1].y;
+          }
           const uint32_t dd = (uint32_t)(d & ~1) * 2u;
 #pragma unroll
           for (int i = 0; i < 32; i += 2) {
@@ -459,6 +426,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
       }
       named_bar(1, 256);
     }
+    if (st == 0) a.cut[blockIdx.x] = cut;
     if (st < kH) bulk_wait0();
   } else if (warp == kMmaWarp) {
     // =================== MMA issuer ===================
@@ -467,7 +435,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
     const uint64_t pv_a0 = sdesc_sw128(kv_base, kBlk, 1024);
     const uint64_t pv_b0 = sdesc_sw128(p_base, kBlk, 1024);
     uint32_t gt = 0, active = 0;
-    while (next_segment(a, walk, sg)) {
+    while (paged_next(a, walk, sg)) {
       if (lane == 0) {
         auto qk_chunk = [&](uint32_t g, int c) {
           const uint32_t slot = (4 * g + c) % kSlots;
@@ -483,23 +451,26 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
         auto kv_phase = [&](uint32_t g, int c) { return ((4 * g + c) / kSlots) & 1u; };
         mbar_wait(bar(kQFull), active & 1u, abort_flag, err);
         tc_fence_after();
-        int qc = 0;
+        int qc = 0;  // chunks of the tile's first product that are issued
         for (int tile = 0; tile < sg.n_tiles; ++tile, ++gt) {
-          for (; qc < 4; ++qc) {
-            mbar_wait(kv_full(gt, qc), kv_phase(gt, qc), abort_flag, err);
-            tc_fence_after();
-            qk_chunk(gt, qc);
+          if (qc < 4) {
+            for (; qc < 4; ++qc) {
+              mbar_wait(kv_full(gt, qc), kv_phase(gt, qc), abort_flag, err);
+              tc_fence_after();
+              fence_async_smem();
+              qk_chunk(gt, qc);
+            }
+            mma_commit(bar(kSFull0 + (gt & 1u)));
           }
-          mma_commit(bar(kSFull));
-          // until P^T comes: as much of the next tile's first product as has
-          // arrived (two chunks at most: the others' slots are this tile's)
+          // until P^T comes: the next tile's first product, as it arrives
           qc = 0;
           const bool more = tile + 1 < sg.n_tiles;
-          while (more && qc < kSlots - 4 && !mbar_test(bar(kPFull), gt & 1u) && !*abort_flag) {
+          while (more && qc < 4 && !mbar_test(bar(kPFull), gt & 1u) && !*abort_flag) {
             if (mbar_test(kv_full(gt + 1, qc), kv_phase(gt + 1, qc))) {
               tc_fence_after();
+              fence_async_smem();
               qk_chunk(gt + 1, qc);
-              ++qc;
+              if (++qc == 4) mma_commit(bar(kSFull0 + ((gt + 1) & 1u)));
             }
           }
           mbar_wait(bar(kPFull), gt & 1u, abort_flag, err);
@@ -529,33 +500,15 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
   } else if (tid < kPtr0) {
     // =================== gather ===================
     const int pt = tid - kPG0;  // 0..127
-    uint32_t gt = 0, done = 0, sent = 0;  // chunks announced / issued
-    auto announce = [&](uint32_t u) {
-      fence_async_smem();
-      mbar_arrive(bar(kKVFull + u % kSlots));
-    };
-    // before a wait that may be long: announce the chunks in flight as they land
-    auto settle = [&]() {
-      if (kFp8) return;
-      if (sent - done >= 3) { cp_async_wait<2>(); announce(done++); }
-      if (sent - done >= 2) { cp_async_wait<1>(); announce(done++); }
-      if (sent - done >= 1) { cp_async_wait<0>(); announce(done++); }
-    };
-    auto wait_for = [&](uint32_t b, uint32_t ph) {
-      if (mbar_test(b, ph)) return;
-      settle();
-      mbar_wait(b, ph, abort_flag, err);
-    };
+    uint32_t gt = 0;
     auto acquire = [&](uint32_t u) {  // chunk u's slot
-      if (u >= kSlots) wait_for(bar(kKVEmpty + u % kSlots), (u / kSlots - 1) & 1u);
+      if (u >= kSlots) mbar_wait(bar(kKVEmpty + u % kSlots), (u / kSlots - 1) & 1u, abort_flag, err);
     };
-    while (next_segment(a, walk, sg)) {
+    while (paged_next(a, walk, sg)) {
       for (int tile = 0; tile < sg.n_tiles; ++tile, ++gt) {
         const uint32_t rs = gt % kAhead;
-        wait_for(bar(kRowFull + rs), (gt / kAhead) & 1u);
+        mbar_wait(bar(kRowFull + rs), (gt / kAhead) & 1u, abort_flag, err);
         const unsigned long long* rp = rows + rs * kKT;
-        // (the softmax of the tile before last is over: a slot of it was reused)
-        if (pt < kKT) vflag[(gt & 1u) * kKT + pt] = rp[pt] != 0;
         if (!kFp8) {
           const int piece = pt & 15;  // 16-byte piece of a row's 256 bytes
           for (int c = 0; c < 4; ++c) {
@@ -568,17 +521,12 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
               const uint16_t* src = reinterpret_cast<const uint16_t*>(rp[row]);
               const uint32_t dst = blk + sw128(row, piece & 7);
               if (src) cp_async16(dst, src + c * 128 + piece * 8);
-              else st_shared_zero16(dst);
+              else cp_async_zero16(dst, a.q);
             }
-            cp_async_commit();
-            ++sent;
-            if (sent - done > 3) {
-              cp_async_wait<3>();
-              announce(done++);
-            }
+            cp_async_arrive(bar(kKVFull + u % kSlots));
           }
         } else {
-          // FP8 rows: a thread takes 16 dims of six rows; the codes of a chunk
+          // FP8 rows: a thread takes 16 dims of four rows; the codes of a chunk
           // are loaded before its slot is waited for, expanded (code times
           // the block's power of two, exact in bf16) and stored.  Rows of the
           // window and the RoPE dims are bf16 and copied as they are.
@@ -586,10 +534,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
           for (int c = 0; c < 4; ++c) {
             const uint32_t u = 4 * gt + c;
             const bool codes = c < 3 || p8 < 4;
-            uint4 w0[6], w1[6];
-            uint32_t sc[6];
+            uint4 w0[4], w1[4];
+            uint32_t sc[4];
 #pragma unroll
-            for (int i = 0; i < 6; ++i) {
+            for (int i = 0; i < 4; ++i) {
               const unsigned long long v = rp[(pt >> 3) + 16 * i];
               const uint8_t* src = reinterpret_cast<const uint8_t*>(v & ~1ull);
               w0[i] = w1[i] = make_uint4(0, 0, 0, 0);
@@ -611,7 +559,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
             const uint32_t blk = kv_base + (u % kSlots) * kSlot + (uint32_t)(p8 >> 2) * kBlk;
             const int q0 = (2 * p8) & 7;  // 16-byte piece of the 128-byte row
 #pragma unroll
-            for (int i = 0; i < 6; ++i) {
+            for (int i = 0; i < 4; ++i) {
               const int row = (pt >> 3) + 16 * i;
               if (codes && (rp[row] & 1ull)) {
                 const float s = mx_scale((int)sc[i]);
@@ -628,19 +576,21 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
               st_shared16(blk + sw128(row, q0), w0[i].x, w0[i].y, w0[i].z, w0[i].w);
               st_shared16(blk + sw128(row, q0 + 1), w1[i].x, w1[i].y, w1[i].z, w1[i].w);
             }
-            announce(u);
+            fence_async_smem();
+            mbar_arrive(bar(kKVFull + u % kSlots));
           }
         }
         mbar_arrive(bar(kRowEmpty + rs));
       }
     }
-    settle();
     cp_async_wait<0>();  // nothing of this block is in flight at exit
   } else {
     // =================== row addresses ===================
-    const int key = tid - kPtr0;  // 0..95
+    const int key = tid - kPtr0;  // 0..63
     uint32_t gt = 0;
-    while (next_segment(a, walk, sg)) {
+    while (paged_next(a, walk, sg)) {
+      // the segment's query into L2 as well, a head a thread
+      if (key < min(kH, a.H - sg.g * kH)) prefetch_l2_bulk(a.q + ((int64_t)sg.b * a.H + sg.g * kH + key) * kD, kD * 2u);
       for (int tile = 0; tile < sg.n_tiles; ++tile, ++gt) {
         const int j = (sg.tile0 + tile) * kKT + key;
         bool fp8 = false;
