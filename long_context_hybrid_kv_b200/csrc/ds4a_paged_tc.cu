@@ -76,6 +76,23 @@ static_assert(kNumBars * 8 <= 320, "barriers");
 constexpr uint32_t kIdescQK = idesc_bf16(128, 64, 0, 0);
 constexpr uint32_t kIdescPV = idesc_bf16(128, 64, 1, 1);
 
+// An MMA / a commit by one elected lane of a converged warp.  The election
+// gives the same lane each time, so that the commits cover the MMAs.
+__device__ __forceinline__ void mma_bf16_elect(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                               uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n elect.sync _|q, 0xffffffff;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void mma_commit_elect(uint32_t bar) {
+  asm volatile(
+      "{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n"
+      " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(bar)
+      : "memory");
+}
+
 // smem -> global, 16-byte aligned, in the thread's bulk group
 __device__ __forceinline__ void bulk_s2g(void* dst, uint32_t src, uint32_t bytes) {
   asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src), "r"(bytes) : "memory");
@@ -97,9 +114,9 @@ __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
 __device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
-// 16 bytes of zeros by the same path
-__device__ __forceinline__ void cp_async_zero16(uint32_t dst, const void* any) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, 0;" ::"r"(dst), "l"(any) : "memory");
+// 16 bytes, or (bytes = 0) zeros without a read
+__device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 
 template <bool kFp8>
@@ -434,68 +451,72 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
     const uint64_t qk_b0 = sdesc_sw128(q_base, 16, 1024);
     const uint64_t pv_a0 = sdesc_sw128(kv_base, kBlk, 1024);
     const uint64_t pv_b0 = sdesc_sw128(p_base, kBlk, 1024);
+    // The whole warp runs this loop and an elected lane issues: with operands
+    // that are the same in all lanes an MMA of this shape goes out every 48
+    // cycles, what its 6 KiB of shared memory take; from a branch of one lane
+    // it was 54 to 90.
     uint32_t gt = 0, active = 0;
     while (paged_next(a, walk, sg)) {
-      if (lane == 0) {
-        auto qk_chunk = [&](uint32_t g, int c) {
-          const uint32_t slot = (4 * g + c) % kSlots;
-          const uint32_t d_s = tmem + (g & 1u) * 64u;
+      auto qk_chunk = [&](uint32_t g, int c) {
+        const uint32_t slot = (4 * g + c) % kSlots;
+        const uint32_t d_s = tmem + (g & 1u) * 64u;
+        const uint64_t da = qk_a0 + ((slot * kSlot) >> 4), db = qk_b0 + ((2u * c * 8192u) >> 4);
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk) {
-            const uint32_t koff = (uint32_t)(kk & 3) * 32u;
-            mma_bf16(d_s, qk_a0 + ((slot * kSlot + (kk >> 2) * kBlk + koff) >> 4),
-                     qk_b0 + (((2u * c + (kk >> 2)) * 8192u + koff) >> 4), kIdescQK, (c | kk) != 0 ? 1u : 0u);
+        for (int kk = 0; kk < 8; ++kk)
+          mma_bf16_elect(d_s, da + (((kk >> 2) * kBlk + (kk & 3) * 32u) >> 4), db + (((kk >> 2) * 8192u + (kk & 3) * 32u) >> 4),
+                         kIdescQK, kk != 0 || c != 0 ? 1u : 0u);
+      };
+      auto kv_full = [&](uint32_t g, int c) { return bar(kKVFull + (4 * g + c) % kSlots); };
+      auto kv_phase = [&](uint32_t g, int c) { return ((4 * g + c) / kSlots) & 1u; };
+      mbar_wait(bar(kQFull), active & 1u, abort_flag, err);
+      tc_fence_after();
+      int qc = 0;  // chunks of the tile's first product that are issued
+      for (int tile = 0; tile < sg.n_tiles; ++tile, ++gt) {
+        if (qc < 4) {
+          for (; qc < 4; ++qc) {
+            mbar_wait(kv_full(gt, qc), kv_phase(gt, qc), abort_flag, err);
+            __syncwarp();
+            tc_fence_after();
+            fence_async_smem();
+            qk_chunk(gt, qc);
           }
-        };
-        auto kv_full = [&](uint32_t g, int c) { return bar(kKVFull + (4 * g + c) % kSlots); };
-        auto kv_phase = [&](uint32_t g, int c) { return ((4 * g + c) / kSlots) & 1u; };
-        mbar_wait(bar(kQFull), active & 1u, abort_flag, err);
-        tc_fence_after();
-        int qc = 0;  // chunks of the tile's first product that are issued
-        for (int tile = 0; tile < sg.n_tiles; ++tile, ++gt) {
-          if (qc < 4) {
-            for (; qc < 4; ++qc) {
-              mbar_wait(kv_full(gt, qc), kv_phase(gt, qc), abort_flag, err);
-              tc_fence_after();
-              fence_async_smem();
-              qk_chunk(gt, qc);
-            }
-            mma_commit(bar(kSFull0 + (gt & 1u)));
-          }
-          // until P^T comes: the next tile's first product, as it arrives
-          qc = 0;
-          const bool more = tile + 1 < sg.n_tiles;
-          while (more && qc < 4 && !mbar_test(bar(kPFull), gt & 1u) && !*abort_flag) {
-            if (mbar_test(kv_full(gt + 1, qc), kv_phase(gt + 1, qc))) {
-              tc_fence_after();
-              fence_async_smem();
-              qk_chunk(gt + 1, qc);
-              if (++qc == 4) mma_commit(bar(kSFull0 + ((gt + 1) & 1u)));
-            }
-          }
-          mbar_wait(bar(kPFull), gt & 1u, abort_flag, err);
-          if (tile == 0 && active > 0) mbar_wait(bar(kEpiDone), (active - 1) & 1u, abort_flag, err);
-          tc_fence_after();
-          const uint32_t acc0 = tile == 0 ? 0u : 1u;
-          for (int c = 0; c < 4; ++c) {
-            const uint32_t slot = (4 * gt + c) % kSlots;
-#pragma unroll
-            for (int kk = 0; kk < kKT / 16; ++kk)
-              mma_bf16(tmem + 128u + 64u * c, pv_a0 + ((slot * kSlot + kk * 2048u) >> 4), pv_b0 + ((kk * 2048u) >> 4),
-                       kIdescPV, kk == 0 ? acc0 : 1u);
-            mma_commit(bar(kKVEmpty + slot));
-          }
-          mma_commit(bar(kPVDone));
+          mma_commit_elect(bar(kSFull0 + (gt & 1u)));
         }
+        // until P^T comes: the next tile's first product, as it arrives
+        qc = 0;
+        const bool more = tile + 1 < sg.n_tiles;
+        while (more && qc < 4) {
+          const bool p_here = mbar_test(bar(kPFull), gt & 1u) || *abort_flag;
+          if (__any_sync(0xffffffffu, p_here)) break;
+          if (__all_sync(0xffffffffu, mbar_test(kv_full(gt + 1, qc), kv_phase(gt + 1, qc)))) {
+            tc_fence_after();
+            fence_async_smem();
+            qk_chunk(gt + 1, qc);
+            if (++qc == 4) mma_commit_elect(bar(kSFull0 + ((gt + 1) & 1u)));
+          }
+        }
+        mbar_wait(bar(kPFull), gt & 1u, abort_flag, err);
+        if (tile == 0 && active > 0) mbar_wait(bar(kEpiDone), (active - 1) & 1u, abort_flag, err);
+        __syncwarp();
+        tc_fence_after();
+        const uint32_t acc0 = tile == 0 ? 0u : 1u;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const uint32_t slot = (4 * gt + c) % kSlots;
+          const uint64_t da = pv_a0 + ((slot * kSlot) >> 4);
+#pragma unroll
+          for (int kk = 0; kk < kKT / 16; ++kk)
+            mma_bf16_elect(tmem + 128u + 64u * c, da + ((kk * 2048u) >> 4), pv_b0 + ((kk * 2048u) >> 4), kIdescPV,
+                           kk == 0 ? acc0 : 1u);
+          mma_commit_elect(bar(kKVEmpty + slot));
+        }
+        mma_commit_elect(bar(kPVDone));
       }
-      __syncwarp();
       ++active;
     }
-    if (lane == 0) {
-      // drain: every MMA issued has finished before the block exits
-      mma_commit(bar(kDrain));
-      mbar_wait(bar(kDrain), 0, abort_flag, err);
-    }
+    // drain: every MMA issued has finished before the block exits
+    mma_commit_elect(bar(kDrain));
+    mbar_wait(bar(kDrain), 0, abort_flag, err);
     __syncwarp();
   } else if (tid < kPtr0) {
     // =================== gather ===================
@@ -510,19 +531,25 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
         mbar_wait(bar(kRowFull + rs), (gt / kAhead) & 1u, abort_flag, err);
         const unsigned long long* rp = rows + rs * kKT;
         if (!kFp8) {
-          const int piece = pt & 15;  // 16-byte piece of a row's 256 bytes
+          // a thread takes the 16-byte piece pt % 16 of eight rows' 256 bytes; a
+          // key without a row gets zeros (no branch: the copies go out together)
+          const int piece = pt & 15;
+          const uint16_t* src[kKT / 8];
+          uint32_t bytes[kKT / 8];
+#pragma unroll
+          for (int i = 0; i < kKT / 8; ++i) {
+            const unsigned long long v = rp[(pt >> 4) + 8 * i];
+            bytes[i] = v ? 16u : 0u;
+            src[i] = (v ? reinterpret_cast<const uint16_t*>(v) : a.q) + piece * 8;
+          }
+          // (rows 8 apart share their place in the swizzle)
+          const uint32_t at = (uint32_t)(piece >> 3) * kBlk + sw128(pt >> 4, piece & 7);
           for (int c = 0; c < 4; ++c) {
             const uint32_t u = 4 * gt + c;
             acquire(u);
-            const uint32_t blk = kv_base + (u % kSlots) * kSlot + (uint32_t)(piece >> 3) * kBlk;
+            const uint32_t dst = kv_base + (u % kSlots) * kSlot + at;
 #pragma unroll
-            for (int i = 0; i < kKT / 8; ++i) {
-              const int row = (pt >> 4) + 8 * i;
-              const uint16_t* src = reinterpret_cast<const uint16_t*>(rp[row]);
-              const uint32_t dst = blk + sw128(row, piece & 7);
-              if (src) cp_async16(dst, src + c * 128 + piece * 8);
-              else cp_async_zero16(dst, a.q);
-            }
+            for (int i = 0; i < kKT / 8; ++i) cp_async16_or_zero(dst + 1024u * i, src[i] + c * 128, bytes[i]);
             cp_async_arrive(bar(kKVFull + u % kSlots));
           }
         } else {
