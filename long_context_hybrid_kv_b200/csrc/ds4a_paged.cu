@@ -35,7 +35,7 @@ __global__ void __launch_bounds__(kGenThreads) paged_attend_generic_kernel(const
   pdl_trigger();
   pdl_wait();
   if (warp == 0) {
-    const PagedRange r = paged_range(a, blockIdx.x);
+    const PagedRange r = paged_range(a, blockIdx.x, kGenKeys);
     if (lane == 0) s_r = r;
   }
   __syncthreads();
@@ -45,7 +45,7 @@ __global__ void __launch_bounds__(kGenThreads) paged_attend_generic_kernel(const
   if (tid == 0) a.cut[blockIdx.x] = make_int4(-1, 0, 0, 0);
   PagedWalk walk(r);
   PagedSegment sg;
-  while (paged_next(a, walk, sg)) {
+  while (paged_next(a, walk, sg, kGenKeys)) {
     const int b = sg.b;
     const PagedSeq& s = sg.seq;
     const int hb = sg.g * kGenHeads, nh = min(kGenHeads, a.H - hb);
@@ -181,121 +181,178 @@ __global__ void __launch_bounds__(kGenThreads) paged_attend_generic_kernel(const
 
 // ---------------------------------------------------------------------------
 // Joining: out = sum_s e^(m_s - M) acc_s / (sum_s e^(m_s - M) l_s + e^(sink -
-// M)) over a cut item's segments s, then the rope slice turned back.  Only
-// cut items are looked at (at most one a block of the attention): every block
-// lists them and takes (item, head) pairs in turn.  Four groups of 64 threads
-// take the segments in turn, a thread eight dims, and are added in order.
-// Bound by L2: an accumulator is read once, half a microsecond or more after
-// it was written.
+// M)) over a cut item's segments s in order, then the rope slice turned back.
+// At most one item is cut behind each block of the attention.  The common
+// item, of up to eight segments, takes a warp a head: the lanes hold the
+// segments' maxima, and a lane sums 16 dims.  An item of more segments (few
+// long sequences) takes a block a head, its warps an eighth of the segments
+// each, added in order.  Bound by latency: three dependent reads from L2 (the
+// cut, the maxima, the accumulators).
 // ---------------------------------------------------------------------------
-constexpr int kJoinThreads = 256, kJoinGroups = 4;
-constexpr int kMaxBlocks = 512;  // of the attention's grid
+constexpr int kJoinWarps = 8, kJoinThreads = 32 * kJoinWarps;
+constexpr int kFewSegments = 8;
 
-__global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_constant__ PagedArgs a) {
-  __shared__ int4 cuts[kMaxBlocks];
-  __shared__ int from[kMaxBlocks];
-  __shared__ float wt[kMaxBlocks];
-  __shared__ int n_cuts;
-  __shared__ float s_l;
-  __shared__ __align__(16) float acc[kJoinGroups][512];
-  const int tid = threadIdx.x, D = a.D;
+// the weights of the segments [s0, s0 + 32) in the lanes: e^(m - M) (0 for
+// one without keys), with M and the denominator's sum L of all segments
+struct JoinHead {
+  float M, L;
+};
+__device__ __forceinline__ const float* join_part(const PagedArgs& a, int c0, int slot0, int s) {
+  return paged_part(a, c0 + s, s == 0 ? slot0 : 0);
+}
+__device__ __forceinline__ JoinHead join_head(const PagedArgs& a, int c0, int slot0, int n_seg, int hl) {
+  const int lane = threadIdx.x & 31;
+  JoinHead j;
+  j.M = -INFINITY;
+  j.L = 0.f;
+  for (int s0 = 0; s0 < n_seg; s0 += 32) {
+    float m = -INFINITY, l = 0.f;
+    if (s0 + lane < n_seg) {
+      const float* p = join_part(a, c0, slot0, s0 + lane);
+      m = p[hl];
+      l = p[a.hn + hl];
+    }
+    float mx = m;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    const float M = fmaxf(j.M, mx);
+    if (M == -INFINITY) continue;
+    j.L = j.L * __expf(j.M - M) + warp_sum(l * __expf(m - M));
+    j.M = M;
+  }
+  return j;
+}
+// 16 dims of a lane: 4 lane + 128 k .. + 3, k < 4 (D <= 512)
+__device__ __forceinline__ void join_sum(const PagedArgs& a, int c0, int slot0, int hl, int s0, int s1, float M,
+                                         float (&x)[16]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) x[i] = 0.f;
+#pragma unroll 4
+  for (int s = s0; s < s1; ++s) {
+    const float* p = join_part(a, c0, slot0, s);
+    const float m = p[hl];
+    float4 v[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (4 * lane + 128 * k < a.D) v[k] = *reinterpret_cast<const float4*>(p + 2 * a.hn + (int64_t)hl * a.D + 4 * lane + 128 * k);
+    }
+    if (m == -INFINITY) continue;  // (a segment without a key that counts may hold anything)
+    const float e = __expf(m - M);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      x[4 * k] = fmaf(v[k].x, e, x[4 * k]);
+      x[4 * k + 1] = fmaf(v[k].y, e, x[4 * k + 1]);
+      x[4 * k + 2] = fmaf(v[k].z, e, x[4 * k + 2]);
+      x[4 * k + 3] = fmaf(v[k].w, e, x[4 * k + 3]);
+    }
+  }
+}
+__device__ __forceinline__ void join_out(const PagedArgs& a, int item, int hl, const JoinHead& j, float (&x)[16]) {
+  const int lane = threadIdx.x & 31, D = a.D;
+  const int b = paged_item_seq(a, item), h = (item - b * a.hgroups) * a.hn + hl;
+  const float sk = a.sink[h];
+  const float inv = j.M == -INFINITY ? 0.f : 1.f / (j.L + __expf(sk - j.M));
+  if (a.weights && lane == 0) {
+    const float top = fmaxf(j.M, sk);
+    a.lse2[(int64_t)item * a.hn + hl] = (top + logf(j.L * expf(j.M - top) + expf(sk - top))) * kLog2e;
+  }
+  const int pos = a.q_pos[b];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int d = 4 * lane + 128 * k;
+    if (d >= D) continue;
+    unsigned int w[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      float x0 = x[4 * k + 2 * i] * inv, x1 = x[4 * k + 2 * i + 1] * inv;
+      const int dd = d + 2 * i;
+      if (dd >= D - a.R) {
+        float cs, sn;
+        rope_cos_sin(pos, a.rope.t[(dd - (D - a.R)) >> 1], &cs, &sn);
+        const float y0 = x0 * cs + x1 * sn;
+        x1 = -x0 * sn + x1 * cs;
+        x0 = y0;
+      }
+      w[i] = f2_to_bf2x2(x0, x1);
+    }
+    *reinterpret_cast<uint2*>(a.out + ((int64_t)b * a.H + h) * D + d) = make_uint2(w[0], w[1]);
+  }
+}
+
+// blocks 0 .. few - 1: eight heads of a cut; from there on: heads of the
+// items of many segments
+__global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_constant__ PagedArgs a, int few) {
+  __shared__ __align__(16) float s_x[kJoinWarps][512];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pdl_trigger();
   pdl_wait();
-  if (tid < 32) {
-    int n = 0;
-    for (int c0 = 0; c0 < a.G; c0 += 32) {
-      const int c = c0 + tid;
-      const int4 v = c < a.G ? a.cut[c] : make_int4(-1, 0, 0, 0);
-      const unsigned int m = __ballot_sync(0xffffffffu, v.x >= 0);
-      if (v.x >= 0) {
-        const int at = n + __popc(m & ((1u << tid) - 1u));
-        cuts[at] = v;
-        from[at] = c;
+  float x[16];
+  if ((int)blockIdx.x < few) {
+    if (a.W == 0)  // sequences without any key: nothing but the sink
+      for (int b = blockIdx.x; b < a.B; b += few) {
+        const PagedSeq s = paged_seq(a, b);
+        if (s.pos >= 0 && s.n_keys == 0)
+          for (int e = tid; e < a.H * a.D / 2; e += kJoinThreads)
+            reinterpret_cast<unsigned int*>(a.out + (int64_t)b * a.H * a.D)[e] = 0u;
       }
-      n += __popc(m);
-    }
-    if (tid == 0) n_cuts = n;
+    const int per = a.hn / kJoinWarps, c0 = blockIdx.x / per, hl = (blockIdx.x - c0 * per) * kJoinWarps + warp;
+    const int4 cut = a.cut[c0];
+    const int n_seg = cut.y - c0 + 1;
+    if (cut.x < 0 || n_seg > kFewSegments) return;
+    const int b = paged_item_seq(a, cut.x);
+    if ((cut.x - b * a.hgroups) * a.hn + hl >= a.H) return;
+    const JoinHead j = join_head(a, c0, cut.z, n_seg, hl);
+    join_sum(a, c0, cut.z, hl, 0, n_seg, j.M, x);
+    join_out(a, cut.x, hl, j, x);
+    return;
   }
-  if (a.W == 0)  // sequences without any key: nothing but the sink
-    for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
-      const PagedSeq s = paged_seq(a, b);
-      if (s.pos >= 0 && s.n_keys == 0)
-        for (int e = tid; e < a.H * D / 2; e += kJoinThreads)
-          reinterpret_cast<unsigned int*>(a.out + (int64_t)b * a.H * D)[e] = 0u;
+  // the (blockIdx.x - few) / hn-th item of many segments
+  const int want = (blockIdx.x - few) / a.hn, hl = (blockIdx.x - few) % a.hn;
+  int seen = 0, c0 = -1;
+  int4 cut = make_int4(-1, 0, 0, 0);
+  for (int c = 0; c < a.G && c0 < 0; c += 160) {
+    int4 v[5];
+#pragma unroll
+    for (int k = 0; k < 5; ++k) v[k] = c + 32 * k + lane < a.G ? a.cut[c + 32 * k + lane] : make_int4(-1, 0, 0, 0);
+#pragma unroll
+    for (int k = 0; k < 5; ++k) {
+      const int ck = c + 32 * k;
+      const unsigned int m = __ballot_sync(0xffffffffu, v[k].x >= 0 && v[k].y - (ck + lane) + 1 > kFewSegments);
+      const int n = __popc(m);
+      if (c0 < 0 && seen + n > want) {
+        unsigned int r = m;
+        for (int i = seen; i < want; ++i) r &= r - 1;
+        const int l = __ffs(r) - 1;
+        c0 = ck + l;
+        cut.x = __shfl_sync(0xffffffffu, v[k].x, l);
+        cut.y = __shfl_sync(0xffffffffu, v[k].y, l);
+        cut.z = __shfl_sync(0xffffffffu, v[k].z, l);
+      }
+      seen += n;
     }
+  }
+  if (c0 < 0) return;
+  const int b = paged_item_seq(a, cut.x), n_seg = cut.y - c0 + 1;
+  if ((cut.x - b * a.hgroups) * a.hn + hl >= a.H) return;
+  const JoinHead j = join_head(a, c0, cut.z, n_seg, hl);
+  join_sum(a, c0, cut.z, hl, warp * n_seg / kJoinWarps, (warp + 1) * n_seg / kJoinWarps, j.M, x);
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    *reinterpret_cast<float4*>(&s_x[warp][4 * lane + 128 * k]) = make_float4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
   __syncthreads();
-  const int grp = tid >> 6, l64 = tid & 63;
-  for (int u = blockIdx.x; u < n_cuts * a.hn; u += gridDim.x) {
-    const int4 cut = cuts[u / a.hn];
-    const int c0 = from[u / a.hn], hl = u % a.hn, n_seg = cut.y - c0 + 1;
-    const int b = cut.x / a.hgroups, h = (cut.x - b * a.hgroups) * a.hn + hl;
-    if (h >= a.H) continue;
-    auto part_of = [&](int s) { return paged_part(a, c0 + s, s == 0 ? cut.z : 0); };
-    __syncthreads();
-    if (tid < 32) {
-      float M = -INFINITY, L = 0.f;
-      for (int s = tid; s < n_seg; s += 32) {
-        wt[s] = part_of(s)[hl];
-        M = fmaxf(M, wt[s]);
-      }
+  if (warp != 0) return;
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-      for (int s = tid; s < n_seg; s += 32) {
-        const float e = M == -INFINITY ? 0.f : __expf(wt[s] - M);
-        wt[s] = e;
-        L = fmaf(part_of(s)[a.hn + hl], e, L);
-      }
-      L = warp_sum(L);
-      if (tid == 0) {
-        const float sk = a.sink[h], top = fmaxf(M, sk);
-        s_l = M == -INFINITY ? 0.f : 1.f / (L + __expf(sk - M));
-        if (a.weights) a.lse2[(int64_t)cut.x * a.hn + hl] = (top + logf(L * expf(M - top) + expf(sk - top))) * kLog2e;
-      }
+  for (int k = 0; k < 4; ++k)
+    for (int w = 1; w < kJoinWarps; ++w) {
+      const float4 v = *reinterpret_cast<const float4*>(&s_x[w][4 * lane + 128 * k]);
+      x[4 * k] += v.x;
+      x[4 * k + 1] += v.y;
+      x[4 * k + 2] += v.z;
+      x[4 * k + 3] += v.w;
     }
-    __syncthreads();
-    const float inv = s_l;
-    const int pos = a.q_pos[b];
-    for (int d0 = 0; d0 < D; d0 += 512) {
-      const int d = d0 + 8 * l64;
-      if (d < D) {
-        float x[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = 0.f;
-#pragma unroll 4
-        for (int s = grp; s < n_seg; s += kJoinGroups) {
-          const float4* p = reinterpret_cast<const float4*>(part_of(s) + 2 * a.hn + (int64_t)hl * D + d);
-          const float4 v = p[0], w = p[1];
-          const float e = wt[s];
-          if (e != 0.f) {  // (a segment without a key that counts may hold anything)
-            x[0] = fmaf(v.x, e, x[0]); x[1] = fmaf(v.y, e, x[1]); x[2] = fmaf(v.z, e, x[2]); x[3] = fmaf(v.w, e, x[3]);
-            x[4] = fmaf(w.x, e, x[4]); x[5] = fmaf(w.y, e, x[5]); x[6] = fmaf(w.z, e, x[6]); x[7] = fmaf(w.w, e, x[7]);
-          }
-        }
-        *reinterpret_cast<float4*>(&acc[grp][8 * l64]) = make_float4(x[0], x[1], x[2], x[3]);
-        *reinterpret_cast<float4*>(&acc[grp][8 * l64 + 4]) = make_float4(x[4], x[5], x[6], x[7]);
-      }
-      __syncthreads();
-      const int e = 2 * tid, dd = d0 + e;
-      if (e < 512 && dd < D) {
-        float x0 = 0.f, x1 = 0.f;
-#pragma unroll
-        for (int g = 0; g < kJoinGroups; ++g) {
-          x0 += acc[g][e];
-          x1 += acc[g][e + 1];
-        }
-        x0 *= inv;
-        x1 *= inv;
-        if (dd >= D - a.R) {
-          float cs, sn;
-          rope_cos_sin(pos, a.rope.t[(dd - (D - a.R)) >> 1], &cs, &sn);
-          const float y0 = x0 * cs + x1 * sn;
-          x1 = -x0 * sn + x1 * cs;
-          x0 = y0;
-        }
-        *reinterpret_cast<unsigned int*>(a.out + ((int64_t)b * a.H + h) * D + dd) = f2_to_bf2x2(x0, x1);
-      }
-    }
-  }
+  join_out(a, cut.x, hl, j, x);
 }
 
 // Attention weight of a slot: sum over the heads of p 2^(ref - lse2), from
@@ -310,10 +367,10 @@ __global__ void __launch_bounds__(kJoinThreads) paged_weights_kernel(const __gri
   const int total = *a.total;
   for (int t = blockIdx.x; t < total; t += gridDim.x) {
     const int2 at = a.tile_of[t];
-    const int b = at.x / a.hgroups;
+    const int b = paged_item_seq(a, at.x);
     if (at.x != b * a.hgroups) continue;  // the sequence's first group sums them all
     const PagedSeq s = paged_seq(a, b);
-    const int n_tiles = paged_tiles(a, s), j0 = at.y * a.kt;
+    const int n_tiles = paged_tiles(s, a.kt), j0 = at.y * a.kt;
     if (at.y == 0 && tid == 0 && s.n > a.w_len) raise_err(a.err, DS4A_DEV_BAD_INDEX);
     __syncthreads();
     for (int h = tid; h < a.H; h += kJoinThreads) {
@@ -328,7 +385,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_weights_kernel(const __gri
         for (int g = 0; g < a.hgroups; ++g) {
           const uint16_t* p = a.tile_p + (((int64_t)t + (int64_t)g * n_tiles) * a.kt + i) * hn;
           for (int c = 8 * q; c < hn; c += 32) {
-            const uint4 v = *reinterpret_cast<const uint4*>(p + c);
+            const uint4 v = *reinterpret_cast<const uint4*>(p + (a.p_swizzled ? c ^ ((i & 7) << 3) : c));
             const unsigned int x[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
@@ -361,7 +418,9 @@ cudaError_t launch_paged_attend_generic(const PagedArgs& a, cudaStream_t s) {
 cudaError_t launch_paged_join(const PagedArgs& a, int tiles, cudaStream_t s) {
   if (a.G > 1 || a.W == 0) {  // (one block cuts nothing)
     TraceScope tr("paged_join", s);
-    const cudaError_t e = launch_pdl(paged_join_kernel, dim3(min(148 * 6, a.G * a.hn)), dim3(kJoinThreads), 0, s, a);
+    const int few = a.G * (a.hn / kJoinWarps), many = (a.G - 1) / kFewSegments * a.hn;
+    // (neighbours share a block, so such an item takes eight blocks or more of its own)
+    const cudaError_t e = launch_pdl(paged_join_kernel, dim3(few + many), dim3(kJoinThreads), 0, s, a, few);
     if (e != cudaSuccess) return e;
   }
   if (!a.weights) return cudaSuccess;
@@ -373,6 +432,7 @@ void paged_shape_generic(PagedArgs* a) {
   a->hn = kGenHeads;
   a->kt = kGenKeys;
   a->G = 148 * 2;
+  a->p_swizzled = 0;
 }
 
 }  // namespace ds4a

@@ -55,6 +55,7 @@ struct PagedArgs {
   int2* tile_of;     // [tiles] item, tile within it (weights only)
   float* tile_ref;   // [tiles][hn] reference of each tile's probabilities, log2 (weights only)
   uint16_t* tile_p;  // [tiles][kt][hn] probabilities against it, bf16 (weights only)
+  int p_swizzled;    // 16-byte piece c of a key's row of tile_p lies at c ^ (key % 8)
   unsigned int* err;
   RopeTheta rope;
 };
@@ -109,7 +110,11 @@ __device__ __forceinline__ const uint8_t* paged_key(const PagedArgs& a, int b, c
   return reinterpret_cast<const uint8_t*>(a.win + (int64_t)b * a.win_bstride + (int64_t)(p % a.win_cap) * a.D);
 }
 
-__device__ __forceinline__ int paged_tiles(const PagedArgs& a, const PagedSeq& s) { return (s.n_keys + a.kt - 1) / a.kt; }
+// (kt: a.kt, as a constant where the caller has one)
+__device__ __forceinline__ int paged_tiles(const PagedSeq& s, int kt) { return (int)((unsigned)(s.n_keys + kt - 1) / (unsigned)kt); }
+__device__ __forceinline__ int paged_item_seq(const PagedArgs& a, int item) {
+  return a.hgroups == 1 ? item : item / a.hgroups;
+}
 
 // Items of at most this many tiles are not cut.
 constexpr int kPagedWhole = 4;
@@ -133,14 +138,14 @@ struct PagedRange {
   int t0, t1;           // this block's tiles
   int item, item_t0;    // the item of tile t0 and the tiles before it
 };
-__device__ __forceinline__ PagedRange paged_range(const PagedArgs& a, int c) {
+__device__ __forceinline__ PagedRange paged_range(const PagedArgs& a, int c, int kt) {
   const int lane = threadIdx.x & 31;
   auto tiles_at = [&](int b0) {
     const int b = b0 + lane;
     if (b >= a.B) return 0;
     const PagedSeq s = paged_seq(a, b);
     if (s.pos < 0 && c == 0) raise_err(a.err, DS4A_DEV_BAD_POS);
-    return paged_tiles(a, s) * a.hgroups;
+    return paged_tiles(s, kt) * a.hgroups;
   };
   auto scan = [&](int v) {
 #pragma unroll
@@ -181,7 +186,7 @@ __device__ __forceinline__ PagedRange paged_range(const PagedArgs& a, int c) {
       if (t >= upto) break;  // (t = total: not found, not moved)
       const int l = __ffs(__ballot_sync(0xffffffffu, before + inc > t)) - 1;
       const int v_l = __shfl_sync(0xffffffffu, v, l), inc_l = __shfl_sync(0xffffffffu, inc, l);
-      const int n = v_l / a.hgroups, b_t0 = before + inc_l - v_l, g = (t - b_t0) / n;
+      const int n = paged_item_seq(a, v_l), b_t0 = before + inc_l - v_l, g = a.hgroups == 1 ? 0 : (t - b_t0) / n;
       const int i_t0 = b_t0 + g * n;
       const int to = n > kPagedWhole ? t : 2 * (t - i_t0) < n ? i_t0 : i_t0 + n;
       if (found == 0) {
@@ -212,13 +217,13 @@ struct PagedSegment {
   int cut_last;  // the item's last block if it begins here and goes on, else -1
   PagedSeq seq;
 };
-__device__ __forceinline__ bool paged_next(const PagedArgs& a, PagedWalk& w, PagedSegment& s) {
+__device__ __forceinline__ bool paged_next(const PagedArgs& a, PagedWalk& w, PagedSegment& s, int kt) {
   while (w.t < w.t1) {
     s.item = w.item;
-    s.b = w.item / a.hgroups;
+    s.b = paged_item_seq(a, w.item);
     s.g = w.item - s.b * a.hgroups;
     s.seq = paged_seq(a, s.b);
-    const int n = paged_tiles(a, s.seq), end = w.item_t0 + n;
+    const int n = paged_tiles(s.seq, kt), end = w.item_t0 + n;
     if (w.t >= end) {  // no tiles
       w.item_t0 = end;
       ++w.item;

@@ -4,20 +4,19 @@
 //
 // All heads read the same rows, so a tile of 64 keys is two dense products with
 // the keys, then the dims, on the MMA's M side and 64 heads on N:
-//   S^T[key][h]  = KV[key][:] . q^[h][:]      K = 512, A K-major, M = 128
-//   O^T[d][h]   += KV[key][d]^T . P^T[key][h]  K = 64 keys, A MN-major
-// M = 128 reads 64 rows past the tile's (whatever lies behind them in shared
-// memory); an A row only reaches its own row of S^T, and those are not looked
-// at.  An MMA of N = 64 is bound by the 6 KiB of shared memory that it reads,
-// so the tile's products take 1.2 us; at 44 GB/s of HBM an SM its rows take
-// 1.5 us.  64 keys, not 128, leave room for nine 128-dim chunks of rows (2.25
-// tiles) next to the 64 KiB of q^, so that the next tile is there and its
-// first product runs during this tile's softmax.
+//   S^T[key][h]  = KV[key][:] . q^[h][:]      K = 512, A K-major, M = 64
+//   O^T[d][h]   += KV[key][d]^T . P^T[key][h]  K = 64 keys, A MN-major, M = 128
+// The products are bound by the shared memory that an MMA reads (32 and 48
+// cycles each): 0.95 us a tile; at 44 GB/s of HBM an SM its rows take 1.5 us.
+// 64 keys, not 128, leave room for nine 128-dim chunks of rows (2.25 tiles)
+// next to the 64 KiB of q^, so that the next tile is there and its first
+// product runs during this tile's softmax.
 //
 // Thread block (one per SM, 480 threads):
 //   warps 0-7    q^ of every segment, softmax, epilogue: two warps per TMEM
-//                lane quarter with 32 heads each; thread = key row of S^T
-//                (the upper two quarters hold none), later dim row of O^T.
+//                lane quarter with 32 heads each.  S^T of M = 64 has 16 keys
+//                in each quarter; a thread holds two keys x 8 heads of it, and
+//                later a dim row of O^T.
 //   warp 8       TMEM allocation; lane 0 issues the MMAs.
 //   warps 9-12   gather the rows by cp.async, a chunk (16 KiB) at a time, into
 //                a ring of nine, in the 128-byte swizzle.  FP8 rows go through
@@ -73,7 +72,7 @@ enum Bar {
 };
 static_assert(kNumBars * 8 <= 320, "barriers");
 
-constexpr uint32_t kIdescQK = idesc_bf16(128, 64, 0, 0);
+constexpr uint32_t kIdescQK = idesc_bf16(64, 64, 0, 0);
 constexpr uint32_t kIdescPV = idesc_bf16(128, 64, 1, 1);
 
 // An MMA / a commit by one elected lane of a converged warp.  The election
@@ -91,6 +90,22 @@ __device__ __forceinline__ void mma_commit_elect(uint32_t bar) {
       "{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n"
       " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(bar)
       : "memory");
+}
+
+// S^T of M = 64: 16 lanes x 32 columns; thread t gets, of each 8 columns j,
+// v[4j], v[4j + 1]: lane t / 4, columns 2 (t % 4), + 1; v[4j + 2], v[4j + 3]:
+// lane t / 4 + 8, the same columns
+__device__ __forceinline__ void tmem_ld_16x32(uint32_t taddr, float (&v)[16]) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+      "[%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
 
 // smem -> global, 16-byte aligned, in the thread's bulk group
@@ -150,7 +165,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
     }
     for (int i = 0; i < kAhead; ++i) {
       mbar_init(bar(kRowFull + i), kKT);
-      mbar_init(bar(kRowEmpty + i), 128 + kKT);  // the gatherers and half of the softmax's key threads
+      mbar_init(bar(kRowEmpty + i), 128 + kKT);  // the gatherers, and 64 softmax threads for all
     }
     mbar_init(bar(kQFull), 256);
     mbar_init(bar(kSFull0), 1);
@@ -165,13 +180,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
     tmem_alloc(smem_u32(tmem_slot), 512);
     tmem_relinquish();
   }
-  pdl_wait();
+  // Positions and queries are inputs that no kernel of the chain writes: the
+  // schedule (unless entries were evicted) and the first q^ are made while the
+  // preceding kernel finishes.
+  if (a.drop != nullptr) pdl_wait();
   if (warp == 0) {
-    const PagedRange r = paged_range(a, blockIdx.x);
-    if (lane == 0) {
-      *s_range = r;
-      if (blockIdx.x == 0) *a.total = r.total;
-    }
+    const PagedRange r = paged_range(a, blockIdx.x, kKT);
+    if (lane == 0) *s_range = r;
   }
   tc_fence_before();
   __syncthreads();
@@ -183,8 +198,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
   if (warp < 8) {
     // =================== q^, softmax, epilogue ===================
     const int q4 = warp & 3, hf = warp >> 2;
-    const int r = 32 * q4 + lane;  // key row of S^T / dim row of O^T within a chunk
-    const bool has_key = q4 < 2;
+    const int r = 32 * q4 + lane;  // dim row of O^T within a chunk
+    const int key0 = 16 * q4 + (lane >> 2), col0 = 2 * (lane & 3);  // keys key0, key0 + 8; columns col0, + 1 of each 8
     const int st = tid;            // 0..255
     const int h0 = 32 * hf;
     const uint32_t t_lane = tmem + ((uint32_t)(32 * q4) << 16);
@@ -192,7 +207,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
     const int R = a.R;
     uint32_t gt = 0;
     int4 cut = make_int4(-1, 0, 0, 0);
-    while (paged_next(a, walk, sg)) {
+    bool waited = false;
+    while (paged_next(a, walk, sg, kKT)) {
       const int nh = min(kH, a.H - sg.g * kH);
       const int64_t head0 = (int64_t)sg.b * a.H + sg.g * kH;
       if (sg.cut_last >= 0) cut = make_int4(sg.item, sg.cut_last, sg.slot, 0);
@@ -263,43 +279,53 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
       }
       fence_async_smem();
       mbar_arrive(bar(kQFull));
-      float lpart[32];
+      if (!waited) pdl_wait();
+      waited = true;
+      float lpart[8];  // columns col0, + 1 of each 8, both keys
 #pragma unroll
-      for (int i = 0; i < 32; ++i) lpart[i] = 0.f;
+      for (int i = 0; i < 8; ++i) lpart[i] = 0.f;
       for (int tile = 0; tile < sg.n_tiles; ++tile, ++gt) {
         mbar_wait(bar(kSFull0 + (gt & 1u)), (gt >> 1) & 1u, abort_flag, err);
         mbar_wait(bar(kRowFull + gt % kAhead), (gt / kAhead) & 1u, abort_flag, err);  // (the tile's addresses)
         tc_fence_after();
-        float z[32];
+        float z[16];
+        tmem_ld_16x32(t_lane + (gt & 1u) * 64u + (uint32_t)h0, z);
+        // a key slot without a row (zero-filled, so its S^T row is 0) gets
+        // -inf through the bias of the scaling FMA
+        const unsigned long long* rp = rows + (gt % kAhead) * kKT + key0;
+        const float ba = rp[0] != 0 ? 0.f : -INFINITY, bb = rp[8] != 0 ? 0.f : -INFINITY;
+        tmem_ld_wait();
+        const float2 sc2 = make_float2(scale2, scale2);
         float lead = -INFINITY;
-        if (has_key) {
-          // a key slot without a row (zero-filled, so its S^T row is 0) gets
-          // -inf through the bias of the scaling FMA
-          const float zbias = rows[(gt % kAhead) * kKT + r] != 0 ? 0.f : -INFINITY;
-          tmem_ld32(t_lane + (gt & 1u) * 64u + (uint32_t)h0, z);
-          tmem_ld_wait();
-          const float4* mrun4 = reinterpret_cast<const float4*>(mrun + h0);
-          const float2 sc2 = make_float2(scale2, scale2), zb2 = make_float2(zbias, zbias);
 #pragma unroll
-          for (int i4 = 0; i4 < 8; ++i4) {
-            const float4 m4 = mrun4[i4];
-            const float2 za = fma_f2(make_float2(z[4 * i4], z[4 * i4 + 1]), sc2, zb2);
-            const float2 zc = fma_f2(make_float2(z[4 * i4 + 2], z[4 * i4 + 3]), sc2, zb2);
-            z[4 * i4] = za.x;
-            z[4 * i4 + 1] = za.y;
-            z[4 * i4 + 2] = zc.x;
-            z[4 * i4 + 3] = zc.y;
-            const float2 da = sub_f2(za, make_float2(m4.x, m4.y)), dc = sub_f2(zc, make_float2(m4.z, m4.w));
-            lead = fmaxf(lead, fmaxf(fmaxf(da.x, da.y), fmaxf(dc.x, dc.y)));
-          }
+        for (int j = 0; j < 4; ++j) {
+          const float2 m2 = *reinterpret_cast<const float2*>(mrun + h0 + 8 * j + col0);
+          const float2 za = fma_f2(make_float2(z[4 * j], z[4 * j + 1]), sc2, make_float2(ba, ba));
+          const float2 zb = fma_f2(make_float2(z[4 * j + 2], z[4 * j + 3]), sc2, make_float2(bb, bb));
+          z[4 * j] = za.x;
+          z[4 * j + 1] = za.y;
+          z[4 * j + 2] = zb.x;
+          z[4 * j + 3] = zb.y;
+          const float2 da = sub_f2(za, m2), db = sub_f2(zb, m2);
+          lead = fmaxf(lead, fmaxf(fmaxf(da.x, da.y), fmaxf(db.x, db.y)));
         }
         const bool rescale = bar_or(1, 256, lead > kRescaleLog2);
-        if (has_key && hf == 0) mbar_arrive(bar(kRowEmpty + gt % kAhead));  // every key thread has read its address
+        if (hf == 0 && lane < 16) mbar_arrive(bar(kRowEmpty + gt % kAhead));  // every thread has read its keys' addresses
         if (rescale) {
-          if (has_key) red[q4 * 64 + h0 + lane] = warp_reduce32<true>(z);
+          // the tile's largest logit of each head (lanes of equal lane % 4)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            float a0 = fmaxf(z[4 * j], z[4 * j + 2]), a1 = fmaxf(z[4 * j + 1], z[4 * j + 3]);
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) {
+              a0 = fmaxf(a0, __shfl_xor_sync(0xffffffffu, a0, o));
+              a1 = fmaxf(a1, __shfl_xor_sync(0xffffffffu, a1, o));
+            }
+            if (lane < 4) *reinterpret_cast<float2*>(red + q4 * 64 + h0 + 8 * j + col0) = make_float2(a0, a1);
+          }
           named_bar(1, 256);
           if (st < kH) {
-            const float mt = fmaxf(red[st], red[64 + st]);
+            const float mt = fmaxf(fmaxf(red[st], red[64 + st]), fmaxf(red[128 + st], red[192 + st]));
             const float mo = mrun[st];
             float al = 1.f;
             if (mt > mo + kRescaleLog2) {  // a -inf tile maximum never moves it
@@ -309,49 +335,44 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
             alpha_s[st] = al;
           }
           named_bar(1, 256);
-          const float4* al4 = reinterpret_cast<const float4*>(alpha_s + h0);
 #pragma unroll
-          for (int i4 = 0; i4 < 8; ++i4) {
-            const float4 a4 = al4[i4];
-            lpart[4 * i4] *= a4.x;
-            lpart[4 * i4 + 1] *= a4.y;
-            lpart[4 * i4 + 2] *= a4.z;
-            lpart[4 * i4 + 3] *= a4.w;
+          for (int j = 0; j < 4; ++j) {
+            const float2 al = *reinterpret_cast<const float2*>(alpha_s + h0 + 8 * j + col0);
+            lpart[2 * j] *= al.x;
+            lpart[2 * j + 1] *= al.y;
           }
         }
         if (a.weights) {
           if (st < kH) a.tile_ref[(int64_t)(sg.t + tile) * kH + st] = mrun[st];
           if (st == 0) a.tile_of[sg.t + tile] = make_int2(sg.item, sg.tile0 + tile);
         }
-        uint32_t pk[16];
-        if (has_key) {
+        uint32_t pa[4], pb[4];
 #pragma unroll
-          for (int i = 0; i < 32; i += 2) {
-            const float2 m2 = reinterpret_cast<const float2*>(mrun + h0)[i >> 1];
-            // a -inf logit gives 0 (the reference is always finite); P is
-            // rounded to bf16 (the MMA's operand) and summed as rounded
-            const float2 d = sub_f2(make_float2(z[i], z[i + 1]), m2);
-            const uint32_t w2 = f2_to_bf2x2(ex2_approx(d.x), ex2_approx(d.y));
-            pk[i >> 1] = w2;
-            const float2 l2 = add_f2(make_float2(lpart[i], lpart[i + 1]), bf2x2_to_f2(w2));
-            lpart[i] = l2.x;
-            lpart[i + 1] = l2.y;
-          }
-          if (a.weights) {
-            uint4* dst = reinterpret_cast<uint4*>(a.tile_p + ((int64_t)(sg.t + tile) * kKT + r) * kH + h0);
-#pragma unroll
-            for (int cc = 0; cc < 4; ++cc) dst[cc] = make_uint4(pk[4 * cc], pk[4 * cc + 1], pk[4 * cc + 2], pk[4 * cc + 3]);
-          }
+        for (int j = 0; j < 4; ++j) {
+          const float2 m2 = *reinterpret_cast<const float2*>(mrun + h0 + 8 * j + col0);
+          // a -inf logit gives 0 (the reference is always finite); P is
+          // rounded to bf16 (the MMA's operand) and summed as rounded
+          const float2 da = sub_f2(make_float2(z[4 * j], z[4 * j + 1]), m2);
+          const float2 db = sub_f2(make_float2(z[4 * j + 2], z[4 * j + 3]), m2);
+          pa[j] = f2_to_bf2x2(ex2_approx(da.x), ex2_approx(da.y));
+          pb[j] = f2_to_bf2x2(ex2_approx(db.x), ex2_approx(db.y));
+          const float2 l2 = add_f2(make_float2(lpart[2 * j], lpart[2 * j + 1]),
+                                   add_f2(bf2x2_to_f2(pa[j]), bf2x2_to_f2(pb[j])));
+          lpart[2 * j] = l2.x;
+          lpart[2 * j + 1] = l2.y;
         }
         if (tile > 0) {
           // the previous tile's PV must be done before P^T and O^T change
           mbar_wait(bar(kPVDone), (gt - 1) & 1u, abort_flag, err);
           tc_fence_after();
         }
-        if (has_key) {
+        // heads h0 + 8j .. + 7 are the 16-byte piece 4 hf + j of the key's row
+        // (key0 and key0 + 8 share their place in the swizzle)
 #pragma unroll
-          for (int cc = 0; cc < 4; ++cc)
-            st_shared16(p_base + sw128(r, 4 * hf + cc), pk[4 * cc], pk[4 * cc + 1], pk[4 * cc + 2], pk[4 * cc + 3]);
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t at = p_base + sw128((uint32_t)key0, (uint32_t)(4 * hf + j)) + 2u * (uint32_t)col0;
+          st_shared32(at, pa[j]);
+          st_shared32(at + 1024u, pb[j]);
         }
         if (tile > 0 && rescale) {
           const float4* al4 = reinterpret_cast<const float4*>(alpha_s + h0);
@@ -381,11 +402,20 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
       // ---------------- epilogue ----------------
       mbar_wait(bar(kPVDone), (gt - 1) & 1u, abort_flag, err);
       tc_fence_after();
-      if (has_key) red[q4 * 64 + h0 + lane] = warp_reduce32<false>(lpart);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        float a0 = lpart[2 * j], a1 = lpart[2 * j + 1];
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) {
+          a0 += __shfl_xor_sync(0xffffffffu, a0, o);
+          a1 += __shfl_xor_sync(0xffffffffu, a1, o);
+        }
+        if (lane < 4) *reinterpret_cast<float2*>(red + q4 * 64 + h0 + 8 * j + col0) = make_float2(a0, a1);
+      }
       named_bar(1, 256);
       float* part = paged_part(a, blockIdx.x, sg.slot);
       if (st < kH) {
-        const float l = red[st] + red[64 + st], m = mrun[st];
+        const float l = red[st] + red[64 + st] + red[128 + st] + red[192 + st], m = mrun[st];
         if (sg.whole) {
           const float den = m <= kNoRef ? 0.f : l + exp2f(sink_s[st] - m);
           inv_s[st] = den > 0.f ? 1.f / den : 0.f;
@@ -443,10 +473,15 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
       }
       named_bar(1, 256);
     }
-    if (st == 0) a.cut[blockIdx.x] = cut;
+    if (!waited) pdl_wait();
+    if (st == 0) {
+      a.cut[blockIdx.x] = cut;
+      if (blockIdx.x == 0) *a.total = s_range->total;
+    }
     if (st < kH) bulk_wait0();
   } else if (warp == kMmaWarp) {
     // =================== MMA issuer ===================
+    pdl_wait();
     const uint64_t qk_a0 = sdesc_sw128(kv_base, 16, 1024);
     const uint64_t qk_b0 = sdesc_sw128(q_base, 16, 1024);
     const uint64_t pv_a0 = sdesc_sw128(kv_base, kBlk, 1024);
@@ -456,7 +491,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
     // cycles, what its 6 KiB of shared memory take; from a branch of one lane
     // it was 54 to 90.
     uint32_t gt = 0, active = 0;
-    while (paged_next(a, walk, sg)) {
+    while (paged_next(a, walk, sg, kKT)) {
       auto qk_chunk = [&](uint32_t g, int c) {
         const uint32_t slot = (4 * g + c) % kSlots;
         const uint32_t d_s = tmem + (g & 1u) * 64u;
@@ -499,6 +534,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
         if (tile == 0 && active > 0) mbar_wait(bar(kEpiDone), (active - 1) & 1u, abort_flag, err);
         __syncwarp();
         tc_fence_after();
+        if (a.weights && lane == 0) {  // P^T as it lies, for the weights
+          bulk_s2g(a.tile_p + (int64_t)(sg.t + tile) * kKT * kH, p_base, kKT * kH * 2);
+          bulk_commit();
+        }
+        __syncwarp();
         const uint32_t acc0 = tile == 0 ? 0u : 1u;
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
@@ -510,6 +550,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
                            kk == 0 ? acc0 : 1u);
           mma_commit_elect(bar(kKVEmpty + slot));
         }
+        if (a.weights) {
+          if (lane == 0) bulk_wait_read0();  // before P^T changes
+          __syncwarp();
+        }
         mma_commit_elect(bar(kPVDone));
       }
       ++active;
@@ -517,15 +561,17 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
     // drain: every MMA issued has finished before the block exits
     mma_commit_elect(bar(kDrain));
     mbar_wait(bar(kDrain), 0, abort_flag, err);
+    if (lane == 0) bulk_wait0();
     __syncwarp();
   } else if (tid < kPtr0) {
     // =================== gather ===================
+    pdl_wait();
     const int pt = tid - kPG0;  // 0..127
     uint32_t gt = 0;
     auto acquire = [&](uint32_t u) {  // chunk u's slot
       if (u >= kSlots) mbar_wait(bar(kKVEmpty + u % kSlots), (u / kSlots - 1) & 1u, abort_flag, err);
     };
-    while (paged_next(a, walk, sg)) {
+    while (paged_next(a, walk, sg, kKT)) {
       for (int tile = 0; tile < sg.n_tiles; ++tile, ++gt) {
         const uint32_t rs = gt % kAhead;
         mbar_wait(bar(kRowFull + rs), (gt / kAhead) & 1u, abort_flag, err);
@@ -613,9 +659,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
     cp_async_wait<0>();  // nothing of this block is in flight at exit
   } else {
     // =================== row addresses ===================
+    pdl_wait();
     const int key = tid - kPtr0;  // 0..63
     uint32_t gt = 0;
-    while (paged_next(a, walk, sg)) {
+    while (paged_next(a, walk, sg, kKT)) {
       // the segment's query into L2 as well, a head a thread
       if (key < min(kH, a.H - sg.g * kH)) prefetch_l2_bulk(a.q + ((int64_t)sg.b * a.H + sg.g * kH + key) * kD, kD * 2u);
       for (int tile = 0; tile < sg.n_tiles; ++tile, ++gt) {
@@ -647,6 +694,7 @@ void paged_shape_tc(PagedArgs* a) {
   a->hn = kH;
   a->kt = kKT;
   a->G = 148;
+  a->p_swizzled = 1;
 }
 
 cudaError_t launch_paged_attend_tc(const PagedArgs& a, cudaStream_t s) {
