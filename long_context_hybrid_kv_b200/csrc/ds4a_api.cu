@@ -557,7 +557,7 @@ static int paged_row_bytes(const ds4a_layer_cfg* cfg, const ds4a_paged_kv* kv) {
 // shape and schedule of a call, and its workspace from `ws` on (nullptr: only
 // the size is wanted)
 static size_t paged_layout(const ds4a_layer_cfg* cfg, const ds4a_paged_kv* kv, int B, int sparse, int weights, void* ws,
-                           PagedArgs* a, int* tiles_out) {
+                           PagedArgs* a) {
   a->B = B; a->H = cfg->n_heads; a->D = cfg->head_dim; a->R = cfg->rope_dim; a->W = cfg->window;
   a->m = cfg->ratio; a->k = cfg->topk; a->cap = kv->max_pages * kv->page_size; a->sparse = sparse;
   // rows of 512 run on the tensor cores, other shapes on the CUDA cores
@@ -574,19 +574,16 @@ static size_t paged_layout(const ds4a_layer_cfg* cfg, const ds4a_paged_kv* kv, i
     at += (bytes + 255) / 256 * 256;
     return p;
   };
-  a->total = reinterpret_cast<int32_t*>(take(4));
   a->cut = reinterpret_cast<int4*>(take((size_t)a->G * sizeof(int4)));
   a->part = reinterpret_cast<float*>(take((size_t)2 * a->G * (2 * a->hn + (size_t)a->hn * a->D) * 4));
   a->lse2 = a->tile_ref = nullptr;
-  a->tile_of = nullptr;
   a->tile_p = nullptr;
   if (weights) {
     a->lse2 = reinterpret_cast<float*>(take((size_t)items * a->hn * 4));
-    a->tile_of = reinterpret_cast<int2*>(take((size_t)tiles * sizeof(int2)));
     a->tile_ref = reinterpret_cast<float*>(take((size_t)tiles * a->hn * 4));
     a->tile_p = reinterpret_cast<uint16_t*>(take((size_t)tiles * a->kt * a->hn * 2));
   }
-  *tiles_out = (int)tiles;
+  a->item_tiles = (int)((keys + a->kt - 1) / a->kt);
   return at;
 }
 
@@ -594,8 +591,7 @@ size_t ds4a_paged_attend_workspace(const ds4a_layer_cfg* cfg, const ds4a_paged_k
                                    int weights) {
   if (check_cfg(cfg) != DS4A_OK || B <= 0 || check_kv(kv, cfg->head_dim, cfg->rope_dim) != DS4A_OK) return 0;
   PagedArgs a;
-  int tiles;
-  return paged_layout(cfg, kv, B, sparse != 0, weights != 0, nullptr, &a, &tiles);
+  return paged_layout(cfg, kv, B, sparse != 0, weights != 0, nullptr, &a);
 }
 
 int ds4a_paged_attend(const ds4a_layer_cfg* cfg, const ds4a_paged_kv* kv, int B, const int32_t* q_pos,
@@ -617,8 +613,7 @@ int ds4a_paged_attend(const ds4a_layer_cfg* cfg, const ds4a_paged_kv* kv, int B,
   if (weights && idx) return DS4A_EUNSUPPORTED;
   if (weights && (w_len < 0 || w_stride < w_len)) return DS4A_EINVAL;
   PagedArgs a;
-  int tiles = 0;
-  const size_t need = paged_layout(cfg, kv, B, idx != nullptr, weights != nullptr, ws, &a, &tiles);
+  const size_t need = paged_layout(cfg, kv, B, idx != nullptr, weights != nullptr, ws, &a);
   if (need == 0) return DS4A_EINVAL;
   if (!ws || ws_bytes < need) return DS4A_ENOSPACE;
   a.scale = cfg->sm_scale; a.eps = cfg->rms_eps;
@@ -633,7 +628,7 @@ int ds4a_paged_attend(const ds4a_layer_cfg* cfg, const ds4a_paged_kv* kv, int B,
   if (!a.err) return DS4A_ECUDA;
   cudaStream_t s = (cudaStream_t)stream;
   const cudaError_t e = paged_tc_supported(a, a.fmt) ? launch_paged_attend_tc(a, s) : launch_paged_attend_generic(a, s);
-  return e != cudaSuccess ? DS4A_ECUDA : cuda_rc(launch_paged_join(a, tiles, s));
+  return e != cudaSuccess ? DS4A_ECUDA : cuda_rc(launch_paged_join(a, s));
 }
 
 int ds4a_paged_append(const ds4a_layer_cfg* cfg, const ds4a_paged_kv* kv, int B, const int32_t* pos,

@@ -41,9 +41,8 @@ __global__ void __launch_bounds__(kGenThreads) paged_attend_generic_kernel(const
   __syncthreads();
   const PagedRange r = s_r;
   const float scale2 = a.scale * kLog2e;
-  if (blockIdx.x == 0 && tid == 0) *a.total = r.total;
   if (tid == 0) a.cut[blockIdx.x] = make_int4(-1, 0, 0, 0);
-  PagedWalk walk(r);
+  PagedRange walk = r;
   PagedSegment sg;
   while (paged_next(a, walk, sg, kGenKeys)) {
     const int b = sg.b;
@@ -80,8 +79,7 @@ __global__ void __launch_bounds__(kGenThreads) paged_attend_generic_kernel(const
     for (int i = 0; i < kAcc; ++i) acc[i] = 0.f;
     for (int i = 0; i < sg.n_tiles; ++i) {
       const int j0 = (sg.tile0 + i) * kGenKeys;
-      const int64_t t = sg.t + i;
-      if (a.weights && tid == 0) a.tile_of[t] = make_int2(sg.item, sg.tile0 + i);
+      const int64_t t = (int64_t)sg.item * a.item_tiles + sg.tile0 + i;
       __syncthreads();
       bool live = false;
       for (int j = warp; j < kGenKeys; j += kGenThreads / 32) {
@@ -183,90 +181,96 @@ __global__ void __launch_bounds__(kGenThreads) paged_attend_generic_kernel(const
 // Joining: out = sum_s e^(m_s - M) acc_s / (sum_s e^(m_s - M) l_s + e^(sink -
 // M)) over a cut item's segments s in order, then the rope slice turned back.
 // At most one item is cut behind each block of the attention.  The common
-// item, of up to eight segments, takes a warp a head: the lanes hold the
-// segments' maxima, and a lane sums 16 dims.  An item of more segments (few
-// long sequences) takes a block a head, its warps an eighth of the segments
-// each, added in order.  Bound by latency: three dependent reads from L2 (the
+// item, of up to eight segments, takes two warps a head: the lanes hold the
+// segments' maxima, and a lane sums 8 dims of half a head.  An item of more
+// segments (few long sequences) takes a block for each half head, its warps an
+// eighth of the segments each, added in order.  Bound by latency: three dependent reads from L2 (the
 // cut, the maxima, the accumulators).
 // ---------------------------------------------------------------------------
 constexpr int kJoinWarps = 8, kJoinThreads = 32 * kJoinWarps;
 constexpr int kFewSegments = 8;
 
-// the weights of the segments [s0, s0 + 32) in the lanes: e^(m - M) (0 for
-// one without keys), with M and the denominator's sum L of all segments
-struct JoinHead {
-  float M, L;
-};
 __device__ __forceinline__ const float* join_part(const PagedArgs& a, int c0, int slot0, int s) {
   return paged_part(a, c0 + s, s == 0 ? slot0 : 0);
 }
-__device__ __forceinline__ JoinHead join_head(const PagedArgs& a, int c0, int slot0, int n_seg, int hl) {
-  const int lane = threadIdx.x & 31;
-  JoinHead j;
+
+// A warp's share of one head: the segments [s0, s1) of n, half of the dims.
+// M, L: maximum and sum over all n segments; x: 8 dims of a lane, d + 128 k ..
+// + 3, d = d0 + 4 lane, k < 2.
+struct JoinSum {
+  float M, L, x[8];
+};
+__device__ __forceinline__ void join_sum(const PagedArgs& a, int c0, int slot0, int n, int hl, int d0, int s0, int s1,
+                                         JoinSum& j) {
+  const int lane = threadIdx.x & 31, d = d0 + 4 * lane;
+  constexpr int kBatch = 4;
+  float4 v[kBatch][2];
+  float m[kBatch];
+  auto load = [&](int s) {  // out before the maxima are known
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      m[i] = -INFINITY;
+      v[i][0] = v[i][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (s + i < s1) {
+        const float* p = join_part(a, c0, slot0, s + i);
+        m[i] = p[hl];
+        if (d < a.D) v[i][0] = *reinterpret_cast<const float4*>(p + 2 * a.hn + (int64_t)hl * a.D + d);
+        if (d + 128 < a.D) v[i][1] = *reinterpret_cast<const float4*>(p + 2 * a.hn + (int64_t)hl * a.D + d + 128);
+      }
+    }
+  };
+  load(s0);
   j.M = -INFINITY;
   j.L = 0.f;
-  for (int s0 = 0; s0 < n_seg; s0 += 32) {
-    float m = -INFINITY, l = 0.f;
-    if (s0 + lane < n_seg) {
-      const float* p = join_part(a, c0, slot0, s0 + lane);
-      m = p[hl];
-      l = p[a.hn + hl];
+  for (int t = 0; t < n; t += 32) {
+    float mt = -INFINITY, lt = 0.f;
+    if (t + lane < n) {
+      const float* p = join_part(a, c0, slot0, t + lane);
+      mt = p[hl];
+      lt = p[a.hn + hl];
     }
-    float mx = m;
+    float mx = mt;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
     const float M = fmaxf(j.M, mx);
     if (M == -INFINITY) continue;
-    j.L = j.L * __expf(j.M - M) + warp_sum(l * __expf(m - M));
+    j.L = j.L * __expf(j.M - M) + warp_sum(lt * __expf(mt - M));
     j.M = M;
   }
-  return j;
-}
-// 16 dims of a lane: 4 lane + 128 k .. + 3, k < 4 (D <= 512)
-__device__ __forceinline__ void join_sum(const PagedArgs& a, int c0, int slot0, int hl, int s0, int s1, float M,
-                                         float (&x)[16]) {
-  const int lane = threadIdx.x & 31;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) x[i] = 0.f;
-#pragma unroll 4
-  for (int s = s0; s < s1; ++s) {
-    const float* p = join_part(a, c0, slot0, s);
-    const float m = p[hl];
-    float4 v[4];
+  for (int i = 0; i < 8; ++i) j.x[i] = 0.f;
+  for (int s = s0; s < s1; s += kBatch) {
+    if (s > s0) load(s);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (4 * lane + 128 * k < a.D) v[k] = *reinterpret_cast<const float4*>(p + 2 * a.hn + (int64_t)hl * a.D + 4 * lane + 128 * k);
-    }
-    if (m == -INFINITY) continue;  // (a segment without a key that counts may hold anything)
-    const float e = __expf(m - M);
+    for (int i = 0; i < kBatch; ++i) {
+      if (m[i] == -INFINITY) continue;  // (a segment without a key that counts may hold anything)
+      const float e = __expf(m[i] - j.M);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      x[4 * k] = fmaf(v[k].x, e, x[4 * k]);
-      x[4 * k + 1] = fmaf(v[k].y, e, x[4 * k + 1]);
-      x[4 * k + 2] = fmaf(v[k].z, e, x[4 * k + 2]);
-      x[4 * k + 3] = fmaf(v[k].w, e, x[4 * k + 3]);
+      for (int k = 0; k < 2; ++k) {
+        j.x[4 * k] = fmaf(v[i][k].x, e, j.x[4 * k]);
+        j.x[4 * k + 1] = fmaf(v[i][k].y, e, j.x[4 * k + 1]);
+        j.x[4 * k + 2] = fmaf(v[i][k].z, e, j.x[4 * k + 2]);
+        j.x[4 * k + 3] = fmaf(v[i][k].w, e, j.x[4 * k + 3]);
+      }
     }
   }
 }
-__device__ __forceinline__ void join_out(const PagedArgs& a, int item, int hl, const JoinHead& j, float (&x)[16]) {
+__device__ __forceinline__ void join_out(const PagedArgs& a, int item, int hl, int d0, const JoinSum& j, int pos, float sk) {
   const int lane = threadIdx.x & 31, D = a.D;
   const int b = paged_item_seq(a, item), h = (item - b * a.hgroups) * a.hn + hl;
-  const float sk = a.sink[h];
   const float inv = j.M == -INFINITY ? 0.f : 1.f / (j.L + __expf(sk - j.M));
-  if (a.weights && lane == 0) {
+  if (a.weights && lane == 0 && d0 == 0) {
     const float top = fmaxf(j.M, sk);
     a.lse2[(int64_t)item * a.hn + hl] = (top + logf(j.L * expf(j.M - top) + expf(sk - top))) * kLog2e;
   }
-  const int pos = a.q_pos[b];
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const int d = 4 * lane + 128 * k;
+  for (int k = 0; k < 2; ++k) {
+    const int d = d0 + 4 * lane + 128 * k;
     if (d >= D) continue;
     unsigned int w[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      float x0 = x[4 * k + 2 * i] * inv, x1 = x[4 * k + 2 * i + 1] * inv;
+      float x0 = j.x[4 * k + 2 * i] * inv, x1 = j.x[4 * k + 2 * i + 1] * inv;
       const int dd = d + 2 * i;
       if (dd >= D - a.R) {
         float cs, sn;
@@ -281,101 +285,103 @@ __device__ __forceinline__ void join_out(const PagedArgs& a, int item, int hl, c
   }
 }
 
-// blocks 0 .. few - 1: eight heads of a cut; from there on: heads of the
-// items of many segments
-__global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_constant__ PagedArgs a, int few) {
-  __shared__ __align__(16) float s_x[kJoinWarps][512];
+// One wave of blocks: each lists the cuts, then their warps take (cut, head,
+// half of the dims) in turn, then the blocks (head, half) of the items of many
+// segments.
+constexpr int kMaxBlocks = 296;  // of the attention's grid
+
+__global__ void __launch_bounds__(kJoinThreads, 3) paged_join_kernel(const __grid_constant__ PagedArgs a) {
+  __shared__ __align__(16) float s_x[kJoinWarps][256];
+  __shared__ int4 s_cut[kMaxBlocks];  // item, first block, segments, slot of the first
+  __shared__ int s_few, s_all;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pdl_trigger();
   pdl_wait();
-  float x[16];
-  if ((int)blockIdx.x < few) {
-    if (a.W == 0)  // sequences without any key: nothing but the sink
-      for (int b = blockIdx.x; b < a.B; b += few) {
-        const PagedSeq s = paged_seq(a, b);
-        if (s.pos >= 0 && s.n_keys == 0)
-          for (int e = tid; e < a.H * a.D / 2; e += kJoinThreads)
-            reinterpret_cast<unsigned int*>(a.out + (int64_t)b * a.H * a.D)[e] = 0u;
-      }
-    const int per = a.hn / kJoinWarps, c0 = blockIdx.x / per, hl = (blockIdx.x - c0 * per) * kJoinWarps + warp;
-    const int4 cut = a.cut[c0];
-    const int n_seg = cut.y - c0 + 1;
-    if (cut.x < 0 || n_seg > kFewSegments) return;
-    const int b = paged_item_seq(a, cut.x);
-    if ((cut.x - b * a.hgroups) * a.hn + hl >= a.H) return;
-    const JoinHead j = join_head(a, c0, cut.z, n_seg, hl);
-    join_sum(a, c0, cut.z, hl, 0, n_seg, j.M, x);
-    join_out(a, cut.x, hl, j, x);
-    return;
-  }
-  // the (blockIdx.x - few) / hn-th item of many segments
-  const int want = (blockIdx.x - few) / a.hn, hl = (blockIdx.x - few) % a.hn;
-  int seen = 0, c0 = -1;
-  int4 cut = make_int4(-1, 0, 0, 0);
-  for (int c = 0; c < a.G && c0 < 0; c += 160) {
-    int4 v[5];
+  if (warp == 0) {  // few segments from the front on, many behind them
+    int4 v[(kMaxBlocks + 31) / 32];
 #pragma unroll
-    for (int k = 0; k < 5; ++k) v[k] = c + 32 * k + lane < a.G ? a.cut[c + 32 * k + lane] : make_int4(-1, 0, 0, 0);
+    for (int k = 0; k < (kMaxBlocks + 31) / 32; ++k) {
+      const int c = 32 * k + lane;
+      v[k] = c < a.G ? a.cut[c] : make_int4(-1, 0, 0, 0);
+    }
+    int at = 0;
 #pragma unroll
-    for (int k = 0; k < 5; ++k) {
-      const int ck = c + 32 * k;
-      const unsigned int m = __ballot_sync(0xffffffffu, v[k].x >= 0 && v[k].y - (ck + lane) + 1 > kFewSegments);
-      const int n = __popc(m);
-      if (c0 < 0 && seen + n > want) {
-        unsigned int r = m;
-        for (int i = seen; i < want; ++i) r &= r - 1;
-        const int l = __ffs(r) - 1;
-        c0 = ck + l;
-        cut.x = __shfl_sync(0xffffffffu, v[k].x, l);
-        cut.y = __shfl_sync(0xffffffffu, v[k].y, l);
-        cut.z = __shfl_sync(0xffffffffu, v[k].z, l);
+    for (int many = 0; many < 2; ++many) {
+#pragma unroll
+      for (int k = 0; k < (kMaxBlocks + 31) / 32; ++k) {
+        const int c = 32 * k + lane, n = v[k].y - c + 1;
+        const bool mine = v[k].x >= 0 && (n > kFewSegments) == (many == 1);
+        const unsigned int m = __ballot_sync(0xffffffffu, mine);
+        if (mine) s_cut[at + __popc(m & ((1u << lane) - 1u))] = make_int4(v[k].x, c, n, v[k].z);
+        at += __popc(m);
       }
-      seen += n;
+      if (lane == 0) (many ? s_all : s_few) = at;
     }
   }
-  if (c0 < 0) return;
-  const int b = paged_item_seq(a, cut.x), n_seg = cut.y - c0 + 1;
-  if ((cut.x - b * a.hgroups) * a.hn + hl >= a.H) return;
-  const JoinHead j = join_head(a, c0, cut.z, n_seg, hl);
-  join_sum(a, c0, cut.z, hl, warp * n_seg / kJoinWarps, (warp + 1) * n_seg / kJoinWarps, j.M, x);
-#pragma unroll
-  for (int k = 0; k < 4; ++k)
-    *reinterpret_cast<float4*>(&s_x[warp][4 * lane + 128 * k]) = make_float4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
+  if (a.W == 0)  // sequences without any key: nothing but the sink
+    for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
+      const PagedSeq s = paged_seq(a, b);
+      if (s.pos >= 0 && s.n_keys == 0)
+        for (int e = tid; e < a.H * a.D / 2; e += kJoinThreads)
+          reinterpret_cast<unsigned int*>(a.out + (int64_t)b * a.H * a.D)[e] = 0u;
+    }
   __syncthreads();
-  if (warp != 0) return;
+  const int few = s_few, all = s_all, halves = a.D > 256 ? 2 : 1, per = a.hn * halves;
+  JoinSum j;
+  for (int u = blockIdx.x * kJoinWarps + warp; u < few * per; u += gridDim.x * kJoinWarps) {
+    const int4 cut = s_cut[u / per];
+    const int w = u % per, hl = w / halves, d0 = (w % halves) * 256;
+    const int b = paged_item_seq(a, cut.x), h = (cut.x - b * a.hgroups) * a.hn + hl;
+    if (h >= a.H) continue;
+    const int pos = a.q_pos[b];
+    const float sk = a.sink[h];
+    join_sum(a, cut.y, cut.w, cut.z, hl, d0, 0, cut.z, j);
+    join_out(a, cut.x, hl, d0, j, pos, sk);
+  }
+  for (int u = few * per + blockIdx.x; u < all * per; u += gridDim.x) {
+    const int4 cut = s_cut[u / per];
+    const int w = u % per, hl = w / halves, d0 = (w % halves) * 256;
+    const int b = paged_item_seq(a, cut.x), h = (cut.x - b * a.hgroups) * a.hn + hl;
+    if (h >= a.H) continue;
+    const int pos = a.q_pos[b];
+    const float sk = a.sink[h];
+    join_sum(a, cut.y, cut.w, cut.z, hl, d0, warp * cut.z / kJoinWarps, (warp + 1) * cut.z / kJoinWarps, j);
+    __syncthreads();
+    *reinterpret_cast<float4*>(&s_x[warp][4 * lane]) = make_float4(j.x[0], j.x[1], j.x[2], j.x[3]);
+    *reinterpret_cast<float4*>(&s_x[warp][4 * lane + 128]) = make_float4(j.x[4], j.x[5], j.x[6], j.x[7]);
+    __syncthreads();
+    if (warp != 0) continue;
 #pragma unroll
-  for (int k = 0; k < 4; ++k)
-    for (int w = 1; w < kJoinWarps; ++w) {
-      const float4 v = *reinterpret_cast<const float4*>(&s_x[w][4 * lane + 128 * k]);
-      x[4 * k] += v.x;
-      x[4 * k + 1] += v.y;
-      x[4 * k + 2] += v.z;
-      x[4 * k + 3] += v.w;
-    }
-  join_out(a, cut.x, hl, j, x);
+    for (int k = 0; k < 2; ++k)
+      for (int q = 1; q < kJoinWarps; ++q) {
+        const float4 y = *reinterpret_cast<const float4*>(&s_x[q][4 * lane + 128 * k]);
+        j.x[4 * k] += y.x;
+        j.x[4 * k + 1] += y.y;
+        j.x[4 * k + 2] += y.z;
+        j.x[4 * k + 3] += y.w;
+      }
+    join_out(a, cut.x, hl, d0, j, pos, sk);
+  }
 }
 
 // Attention weight of a slot: sum over the heads of p 2^(ref - lse2), from
-// the probabilities that the attention left per tile (128 bytes a key for 64
-// heads).  A block a tile; the factors 2^(ref - lse2) once a tile, four
+// the probabilities that the attention left per tile.  A block a tile; the factors 2^(ref - lse2) once a tile, four
 // threads a key.
 __global__ void __launch_bounds__(kJoinThreads) paged_weights_kernel(const __grid_constant__ PagedArgs a) {
   __shared__ float f[128];
   const int tid = threadIdx.x, hn = a.hn;
   pdl_trigger();
   pdl_wait();
-  const int total = *a.total;
-  for (int t = blockIdx.x; t < total; t += gridDim.x) {
-    const int2 at = a.tile_of[t];
-    const int b = paged_item_seq(a, at.x);
-    if (at.x != b * a.hgroups) continue;  // the sequence's first group sums them all
+  for (int u = blockIdx.x; u < a.B * a.item_tiles; u += gridDim.x) {
+    const int b = u / a.item_tiles, tile = u - b * a.item_tiles, j0 = tile * a.kt;
+    const int item = b * a.hgroups;
     const PagedSeq s = paged_seq(a, b);
-    const int n_tiles = paged_tiles(s, a.kt), j0 = at.y * a.kt;
-    if (at.y == 0 && tid == 0 && s.n > a.w_len) raise_err(a.err, DS4A_DEV_BAD_INDEX);
+    if (tile == 0 && tid == 0 && s.n > a.w_len) raise_err(a.err, DS4A_DEV_BAD_INDEX);
+    if (j0 >= min(s.n, a.w_len)) continue;
     __syncthreads();
     for (int h = tid; h < a.H; h += kJoinThreads) {
       const int g = h / hn;
-      f[h] = exp2f(a.tile_ref[((int64_t)t + (int64_t)g * n_tiles) * hn + h % hn] - a.lse2[(int64_t)(at.x + g) * hn + h % hn]);
+      f[h] = exp2f(a.tile_ref[((int64_t)(item + g) * a.item_tiles + tile) * hn + h % hn] - a.lse2[(int64_t)(item + g) * hn + h % hn]);
     }
     __syncthreads();
     for (int i0 = 0; i0 < a.kt; i0 += kJoinThreads / 4) {
@@ -383,9 +389,9 @@ __global__ void __launch_bounds__(kJoinThreads) paged_weights_kernel(const __gri
       float w = 0.f;
       if (i < a.kt)
         for (int g = 0; g < a.hgroups; ++g) {
-          const uint16_t* p = a.tile_p + (((int64_t)t + (int64_t)g * n_tiles) * a.kt + i) * hn;
+          const uint16_t* p = a.tile_p + (((int64_t)(item + g) * a.item_tiles + tile) * a.kt + i) * hn;
           for (int c = 8 * q; c < hn; c += 32) {
-            const uint4 v = *reinterpret_cast<const uint4*>(p + (a.p_swizzled ? c ^ ((i & 7) << 3) : c));
+            const uint4 v = *reinterpret_cast<const uint4*>(p + c);
             const unsigned int x[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
@@ -404,6 +410,66 @@ __global__ void __launch_bounds__(kJoinThreads) paged_weights_kernel(const __gri
   }
 }
 
+// The same for the tensor-core kernel's tiles (64 keys x 64 heads, swizzled),
+// a warp a tile and no block barrier: a load covers four keys' rows, lane l
+// the piece l % 8 of key l / 8, so that a lane's heads alternate between two
+// sets of eight.
+__global__ void __launch_bounds__(kJoinThreads) paged_weights64_kernel(const __grid_constant__ PagedArgs a) {
+  __shared__ __align__(16) float fs[kJoinWarps][64];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = lane >> 3, piece = lane & 7;
+  pdl_trigger();
+  pdl_wait();
+  float* f = fs[warp];
+  for (int u = blockIdx.x * kJoinWarps + warp; u < a.B * a.item_tiles; u += gridDim.x * kJoinWarps) {
+    const int b = u / a.item_tiles, tile = u - b * a.item_tiles, j0 = tile * 64;
+    const PagedSeq s = paged_seq(a, b);
+    if (tile == 0 && lane == 0 && s.n > a.w_len) raise_err(a.err, DS4A_DEV_BAD_INDEX);
+    const int n = min(s.n, a.w_len);
+    if (j0 >= n) continue;
+    float w[2] = {0.f, 0.f};  // of the keys 32 i + 4 piece + row
+    for (int g = 0; g < a.hgroups; ++g) {
+      const int64_t item = (int64_t)b * a.hgroups + g, t = item * a.item_tiles + tile;
+      const uint4* p = reinterpret_cast<const uint4*>(a.tile_p + t * 64 * 64) + lane;
+      uint4 v[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) v[i] = p[32 * i];
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int h = lane + 32 * i;
+        f[h] = g * 64 + h < a.H ? exp2f(a.tile_ref[t * 64 + h] - a.lse2[item * 64 + h]) : 0.f;
+      }
+      __syncwarp();
+      float f0[8], f1[8];  // keys 8k + row: piece ^ row; keys 8k + 4 + row: piece ^ (4 + row)
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        f0[q] = f[8 * (piece ^ row) + q];
+        f1[q] = f[8 * (piece ^ (row + 4)) + q];
+      }
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const unsigned int y[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+        float z = 0.f;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const float2 x = bf2x2_to_f2(y[q]);
+          z = fmaf(x.x, i & 1 ? f1[2 * q] : f0[2 * q], z);
+          z = fmaf(x.y, i & 1 ? f1[2 * q + 1] : f0[2 * q + 1], z);
+        }
+        z += __shfl_xor_sync(0xffffffffu, z, 1);
+        z += __shfl_xor_sync(0xffffffffu, z, 2);
+        z += __shfl_xor_sync(0xffffffffu, z, 4);
+        if (piece == (i & 7)) w[i >> 3] += z;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int j = j0 + 32 * i + 4 * piece + row;
+      if (j < n) a.weights[(int64_t)b * a.w_stride + j] = f2bf(w[i]);
+    }
+  }
+}
+
 }  // namespace
 
 cudaError_t launch_paged_attend_generic(const PagedArgs& a, cudaStream_t s) {
@@ -415,24 +481,27 @@ cudaError_t launch_paged_attend_generic(const PagedArgs& a, cudaStream_t s) {
   return launch_pdl(paged_attend_generic_kernel, dim3(a.G), dim3(kGenThreads), smem, s, a);
 }
 
-cudaError_t launch_paged_join(const PagedArgs& a, int tiles, cudaStream_t s) {
-  if (a.G > 1 || a.W == 0) {  // (one block cuts nothing)
+cudaError_t launch_paged_join(const PagedArgs& a, cudaStream_t s) {
+  if (a.item_tiles > kPagedWhole || a.W == 0) {  // else nothing is cut
     TraceScope tr("paged_join", s);
-    const int few = a.G * (a.hn / kJoinWarps), many = (a.G - 1) / kFewSegments * a.hn;
-    // (neighbours share a block, so such an item takes eight blocks or more of its own)
-    const cudaError_t e = launch_pdl(paged_join_kernel, dim3(few + many), dim3(kJoinThreads), 0, s, a, few);
+    const int blocks = (a.G * a.hn * 2 + kJoinWarps - 1) / kJoinWarps;
+    const cudaError_t e = launch_pdl(paged_join_kernel, dim3(min(148 * 3, blocks)), dim3(kJoinThreads), 0, s, a);
     if (e != cudaSuccess) return e;
   }
   if (!a.weights) return cudaSuccess;
   TraceScope tr("paged_weights", s);
-  return launch_pdl(paged_weights_kernel, dim3(min(tiles, 148 * 6)), dim3(kJoinThreads), 0, s, a);
+  const int64_t tiles = (int64_t)a.B * a.item_tiles;
+  if (a.hn == 64) {
+    const int64_t blocks = (tiles + kJoinWarps - 1) / kJoinWarps;
+    return launch_pdl(paged_weights64_kernel, dim3((int)(blocks < 148 * 2 ? blocks : 148 * 2)), dim3(kJoinThreads), 0, s, a);
+  }
+  return launch_pdl(paged_weights_kernel, dim3((int)(tiles < 148 * 8 ? tiles : 148 * 8)), dim3(kJoinThreads), 0, s, a);
 }
 
 void paged_shape_generic(PagedArgs* a) {
   a->hn = kGenHeads;
   a->kt = kGenKeys;
   a->G = 148 * 2;
-  a->p_swizzled = 0;
 }
 
 }  // namespace ds4a

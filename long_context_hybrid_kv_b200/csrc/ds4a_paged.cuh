@@ -6,16 +6,21 @@
 // 0 .. n - 1 of its pages.  Its keys are those slots (or the listed ones)
 // and then the window rows.
 //
-// Work is counted in tiles of kt keys.  The tiles of all items (sequence,
-// group of hn heads) stand in one row, item after item, and are cut into as
-// many equal ranges as there are blocks, so that every block gets the same
-// number of tiles (give or take one) whatever the lengths are, and the host
-// needs to know none of them: a captured launch serves growing sequences.
+// Work is counted in tiles of kt keys; an item is a sequence and a group of hn
+// heads.  The host knows no length, so a captured launch serves growing
+// sequences: every block of the attention finds its own place.
+//   Up to as many items as blocks: the shortest T for which the blocks do when
+//   an item of n tiles is cut into ceil(n / T) equal pieces, a block each, and
+//   items of up to T / 2 tiles share blocks, whole, each counted three tiles
+//   longer: that is about what a segment costs besides its tiles (its q^, the
+//   filling of the pipeline, the output), and why pieces a little longer than
+//   the average beat equal shares.  A piece costs, on top, a float accumulator
+//   written (128 KiB for 64 heads x 512) and read by the joining kernel.
+//   More items, or lengths with which T would exceed the average by more than
+//   a segment's cost: their tiles stand in one row, cut into equal ranges, but
+//   a cut that would fall into a short item moves to its nearer end.
 // A block's piece of an item is a segment; an item that one block holds whole
-// is finished there, the others are joined from their segments.  As a segment
-// costs its block a float accumulator written (128 KiB for 64 heads x 512) and
-// the joining kernel one read, a cut that would fall into a short item moves
-// to its nearer end, and a block gets at least two tiles.
+// is finished there, the others are joined from their segments.
 #pragma once
 
 #include "ds4a_internal.cuh"
@@ -48,14 +53,13 @@ struct PagedArgs {
   int w_len;
   // schedule and workspace
   int hn, hgroups, kt, G;
-  int32_t* total;    // tiles of all items
   int4* cut;         // [G] the item that begins in the block and is cut: item or -1, its last block, its slot
   float* part;       // [2 G][2 hn + hn D] segments: max (natural log), sum, accumulator
   float* lse2;       // [items][hn] log2 of the softmax denominator (weights only)
-  int2* tile_of;     // [tiles] item, tile within it (weights only)
-  float* tile_ref;   // [tiles][hn] reference of each tile's probabilities, log2 (weights only)
-  uint16_t* tile_p;  // [tiles][kt][hn] probabilities against it, bf16 (weights only)
-  int p_swizzled;    // 16-byte piece c of a key's row of tile_p lies at c ^ (key % 8)
+  int item_tiles;    // at most that many tiles an item
+  float* tile_ref;   // [items][item_tiles][hn] reference of each tile's probabilities, log2 (weights only)
+  uint16_t* tile_p;  // [items][item_tiles][kt][hn] probabilities against it, bf16 (weights only); of the
+                     // tensor-core kernel the 16-byte piece c of a key's row at c ^ (key % 8)
   unsigned int* err;
   RopeTheta rope;
 };
@@ -116,11 +120,13 @@ __device__ __forceinline__ int paged_item_seq(const PagedArgs& a, int item) {
   return a.hgroups == 1 ? item : item / a.hgroups;
 }
 
-// Items of at most this many tiles are not cut.
-constexpr int kPagedWhole = 4;
+// Items of at most this many tiles are not cut, and no piece is shorter.
+constexpr int kPagedWhole = 4, kPagedLeast = 2;
+constexpr int kPagedCost = 3;  // of a segment, in tiles
+constexpr int kPagedChunks = 8;  // of 32 sequences, that a warp holds in registers (296 blocks at most)
 
-// The blocks that take part, where block c's range begins before its ends
-// are moved, and the block that holds tile t.
+// More items than blocks: the blocks that take part, where block c's range
+// begins before its ends are moved, and the block that holds tile t.
 __device__ __forceinline__ int paged_blocks(int total, int G) { return min(G, (total + 1) / 2); }
 __device__ __forceinline__ int paged_start(int c, int total, int ge) {
   const unsigned q = (unsigned)total / (unsigned)ge, rem = (unsigned)total - q * (unsigned)ge;
@@ -131,21 +137,23 @@ __device__ __forceinline__ int paged_block_of(int t, int total, int ge) {
   return (unsigned)t < wide ? (int)((unsigned)t / (q + 1)) : (int)(rem + ((unsigned)t - wide) / q);
 }
 
-// A block's place in the schedule, found by one warp (all 32 lanes): the
-// tiles before every item are summed 32 sequences at a time.
+// A block's place in the schedule, found by one warp (all 32 lanes).
 struct PagedRange {
-  int total, ge, raw0;  // tiles of all items, blocks that take part, start before moving
-  int t0, t1;           // this block's tiles
-  int item, item_t0;    // the item of tile t0 and the tiles before it
+  int kind;           // 0: a piece of an item, 1: whole items that share the block, 2: a range of the row of all tiles
+  int item;           // the first
+  int t0, t1;         // 0: tiles of the item.  2: tiles of the row
+  int last;           // 0: the item's last block
+  int T, stop, done;  // 1: items above T / 2 are left out; twice the cost at which to stop, cost before the first
+  int item_t0, raw0, total, ge;  // 2: tiles before the first item, start before moving, tiles and blocks in all
 };
 __device__ __forceinline__ PagedRange paged_range(const PagedArgs& a, int c, int kt) {
-  const int lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31, hg = a.hgroups, items = a.B * hg;
   auto tiles_at = [&](int b0) {
     const int b = b0 + lane;
     if (b >= a.B) return 0;
     const PagedSeq s = paged_seq(a, b);
     if (s.pos < 0 && c == 0) raise_err(a.err, DS4A_DEV_BAD_POS);
-    return paged_tiles(s, kt) * a.hgroups;
+    return paged_tiles(s, kt);
   };
   auto scan = [&](int v) {
 #pragma unroll
@@ -155,30 +163,127 @@ __device__ __forceinline__ PagedRange paged_range(const PagedArgs& a, int c, int
     }
     return v;
   };
+  auto sum = [&](int v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+  };
   PagedRange r;
-  int v = 0, inc = 0, total = 0;
+  r.kind = 1;
+  r.item = items;  // nothing to do
+  r.t0 = r.t1 = r.last = r.T = r.stop = r.done = r.item_t0 = r.raw0 = r.total = r.ge = 0;
+  int total = 0;
+  bool rows = false;
+  if (items <= a.G) {
+    int n[kPagedChunks], most = 0;
+#pragma unroll
+    for (int k = 0; k < kPagedChunks; ++k) {
+      n[k] = 0;
+      if (32 * k >= a.B) break;
+      n[k] = tiles_at(32 * k);
+      total += n[k] * hg;
+      most = max(most, n[k]);
+    }
+    total = sum(total);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
+    int T = 0;
+    auto pieces = [&](int v) {  // 0: none, or small
+      return 2 * v <= T ? 0 : v <= kPagedWhole ? 1 : (int)((unsigned)(v + T - 1) / (unsigned)T);
+    };
+    auto cost = [&](int v) { return v > 0 && 2 * v <= T ? v + kPagedCost : 0; };
+    int big = 0, small = 0;
+    auto fits = [&](int t) {
+      T = t;
+      big = small = 0;
+#pragma unroll
+      for (int k = 0; k < kPagedChunks; ++k) {
+        if (32 * k >= a.B) break;
+        big += pieces(n[k]) * hg;
+        small += cost(n[k]) * hg;
+      }
+      big = sum(big);
+      small = sum(small);
+      return big + (small + T + kPagedCost - 1) / (T + kPagedCost) <= a.G;
+    };
+    // (T = the longest item's tiles fits: one block an item or fewer)
+    int yes = max(kPagedLeast, (total + a.G - 1) / a.G);
+    if (!fits(yes)) {
+      int no = yes;
+      yes = max(most, no + 1);
 #pragma unroll 1
-  for (int b0 = 0; b0 < a.B; b0 += 32) {
-    v = tiles_at(b0);
-    inc = scan(v);
-    total += __shfl_sync(0xffffffffu, inc, 31);
+      while (yes - no > 1) {
+        const int mid = (yes + no) >> 1;
+        if (fits(mid)) yes = mid;
+        else no = mid;
+      }
+      fits(yes);
+    }
+    // (lengths that do not fit well: the row of tiles is better, although its
+    // blocks have two segments)
+    rows = T > (total + a.G - 1) / a.G + kPagedCost && most > kPagedWhole;
+    int blocks = 0, before = 0;
+    const int share = T + kPagedCost, s0 = (c - big) * 2 * share;  // a shared block takes the items whose middle lies in its share
+    r.T = T;
+    r.stop = s0 + 2 * share;
+    bool found = false;
+#pragma unroll
+    for (int k = 0; k < kPagedChunks; ++k) {
+      if (32 * k >= a.B || rows) break;
+      const int p = pieces(n[k]) * hg, w = cost(n[k]);
+      if (c < big) {
+        const int pi = scan(p);
+        const unsigned int here = __ballot_sync(0xffffffffu, blocks + pi > c);
+        if (here && !found) {
+          found = true;
+          const int l = __ffs(here) - 1;
+          const int n_l = __shfl_sync(0xffffffffu, n[k], l), p_l = __shfl_sync(0xffffffffu, p, l) / hg;
+          const int at = c - blocks - __shfl_sync(0xffffffffu, pi - p, l), g = at / p_l, j = at - g * p_l;
+          r.kind = 0;
+          r.item = (32 * k + l) * hg + g;
+          r.t0 = (int)((unsigned)(j * n_l) / (unsigned)p_l);
+          r.t1 = (int)((unsigned)((j + 1) * n_l) / (unsigned)p_l);
+          r.last = c - j + p_l - 1;
+        }
+        blocks += __shfl_sync(0xffffffffu, pi, 31);
+      } else {
+        const int wi = scan(w * hg);
+        // the sequence's last group lies behind the share's begin
+        const int end2 = 2 * (before + wi) - w;
+        const unsigned int here = __ballot_sync(0xffffffffu, w > 0 && end2 >= s0);
+        if (here && !found) {
+          found = true;
+          const int l = __ffs(here) - 1;
+          int g = 0, d = before + __shfl_sync(0xffffffffu, wi - w * hg, l);
+          const int w_l = __shfl_sync(0xffffffffu, w, l);
+          for (; 2 * d + w_l < s0; d += w_l) ++g;
+          r.item = (32 * k + l) * hg + g;
+          r.done = d;
+        }
+        before += __shfl_sync(0xffffffffu, wi, 31);
+      }
+    }
+    if (!rows) return r;
+  }
+  r.kind = 2;
+  int v = 0, inc = 0;
+  if (items > a.G) {
+#pragma unroll 1
+    for (int b0 = 0; b0 < a.B; b0 += 32) total += sum(tiles_at(b0)) * hg;
   }
   r.total = total;
   r.ge = max(1, paged_blocks(total, a.G));
   r.raw0 = paged_start(c, total, r.ge);
   r.t0 = r.raw0;
   r.t1 = paged_start(c + 1, total, r.ge);
-  r.item = a.B * a.hgroups;
   r.item_t0 = total;
   if (r.t0 >= r.t1) return r;
   // an end that lies in a short item moves to the nearer end of it
   int before = 0, found = 0;
 #pragma unroll 1
   for (int b0 = 0; b0 < a.B && found < 2; b0 += 32) {
-    if (a.B > 32) {
-      v = tiles_at(b0);
-      inc = scan(v);
-    }
+    v = tiles_at(b0) * hg;
+    inc = scan(v);
     const int upto = before + __shfl_sync(0xffffffffu, inc, 31);
 #pragma unroll 1
     while (found < 2) {
@@ -186,12 +291,12 @@ __device__ __forceinline__ PagedRange paged_range(const PagedArgs& a, int c, int
       if (t >= upto) break;  // (t = total: not found, not moved)
       const int l = __ffs(__ballot_sync(0xffffffffu, before + inc > t)) - 1;
       const int v_l = __shfl_sync(0xffffffffu, v, l), inc_l = __shfl_sync(0xffffffffu, inc, l);
-      const int n = paged_item_seq(a, v_l), b_t0 = before + inc_l - v_l, g = a.hgroups == 1 ? 0 : (t - b_t0) / n;
+      const int n = paged_item_seq(a, v_l), b_t0 = before + inc_l - v_l, g = hg == 1 ? 0 : (t - b_t0) / n;
       const int i_t0 = b_t0 + g * n;
       const int to = n > kPagedWhole ? t : 2 * (t - i_t0) < n ? i_t0 : i_t0 + n;
       if (found == 0) {
         r.t0 = to;
-        r.item = (b0 + l) * a.hgroups + g + (to == i_t0 + n ? 1 : 0);
+        r.item = (b0 + l) * hg + g + (to == i_t0 + n ? 1 : 0);
         r.item_t0 = to == i_t0 + n ? to : i_t0;
       } else {
         r.t1 = to;
@@ -203,43 +308,60 @@ __device__ __forceinline__ PagedRange paged_range(const PagedArgs& a, int c, int
   return r;
 }
 
-// The segments of a block one after the other.
-struct PagedWalk {
-  int t, t1, item, item_t0, raw0, total, ge;
-  __device__ __forceinline__ explicit PagedWalk(const PagedRange& r)
-      : t(r.t0), t1(r.t1), item(r.item), item_t0(r.item_t0), raw0(r.raw0), total(r.total), ge(r.ge) {}
-};
+// The segments of a block one after the other: paged_next takes the next one.
 struct PagedSegment {
   int item, b, g;
-  int t, tile0, n_tiles;  // first tile in the row of all tiles and in the item; how many
+  int tile0, n_tiles;  // first tile in the item; how many
   bool whole;
-  int slot;      // of a partial result: 0 if the item began in an earlier block, else 1
+  int slot;      // of a partial result: 1 if the item begins behind the start of the block's range, else 0
   int cut_last;  // the item's last block if it begins here and goes on, else -1
   PagedSeq seq;
 };
-__device__ __forceinline__ bool paged_next(const PagedArgs& a, PagedWalk& w, PagedSegment& s, int kt) {
-  while (w.t < w.t1) {
+__device__ __forceinline__ bool paged_next(const PagedArgs& a, PagedRange& w, PagedSegment& s, int kt) {
+  const int items = a.B * a.hgroups;
+  while (w.item < items) {
     s.item = w.item;
     s.b = paged_item_seq(a, w.item);
     s.g = w.item - s.b * a.hgroups;
+    if (w.kind == 2 && w.t0 >= w.t1) return false;
     s.seq = paged_seq(a, s.b);
-    const int n = paged_tiles(s.seq, kt), end = w.item_t0 + n;
-    if (w.t >= end) {  // no tiles
-      w.item_t0 = end;
-      ++w.item;
-      continue;
+    const int n = paged_tiles(s.seq, kt);
+    s.slot = 0;
+    s.cut_last = -1;
+    if (w.kind == 0) {
+      s.tile0 = w.t0;
+      s.n_tiles = w.t1 - w.t0;
+      s.whole = s.n_tiles == n;
+      if (s.tile0 == 0 && !s.whole) s.cut_last = w.last;
+      w.item = items;
+      return true;
     }
-    const int stop = min(w.t1, end);
-    s.t = w.t;
-    s.tile0 = w.t - w.item_t0;
-    s.n_tiles = stop - w.t;
-    s.whole = s.n_tiles == n;
-    s.slot = w.item_t0 > w.raw0 ? 1 : 0;
-    s.cut_last = s.tile0 == 0 && !s.whole ? paged_block_of(end - 1, w.total, w.ge) : -1;
-    w.t = stop;
-    w.item_t0 = end;
     ++w.item;
-    return true;
+    if (w.kind == 1) {
+      if (n == 0 || 2 * n > w.T) continue;
+      const int cost = n + kPagedCost;
+      if (2 * w.done + cost >= w.stop) {
+        w.item = items;
+        return false;
+      }
+      w.done += cost;
+      s.tile0 = 0;
+      s.n_tiles = n;
+      s.whole = true;
+      return true;
+    }
+    const int end = w.item_t0 + n, stop = min(w.t1, end);
+    if (w.t0 < end) {
+      s.tile0 = w.t0 - w.item_t0;
+      s.n_tiles = stop - w.t0;
+      s.whole = s.n_tiles == n;
+      s.slot = w.item_t0 > w.raw0 ? 1 : 0;
+      if (s.tile0 == 0 && !s.whole) s.cut_last = paged_block_of(end - 1, w.total, w.ge);
+      w.t0 = stop;
+      w.item_t0 = end;
+      return true;
+    }
+    w.item_t0 = end;  // no tiles
   }
   return false;
 }
@@ -253,7 +375,6 @@ void paged_shape_tc(PagedArgs* a);
 bool paged_tc_supported(const PagedArgs& a, int fmt);
 cudaError_t launch_paged_attend_generic(const PagedArgs& a, cudaStream_t s);
 cudaError_t launch_paged_attend_tc(const PagedArgs& a, cudaStream_t s);
-// tiles: at most that many
-cudaError_t launch_paged_join(const PagedArgs& a, int tiles, cudaStream_t s);
+cudaError_t launch_paged_join(const PagedArgs& a, cudaStream_t s);
 
 }  // namespace ds4a

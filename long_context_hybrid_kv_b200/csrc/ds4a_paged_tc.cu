@@ -51,7 +51,7 @@ constexpr uint32_t kOffQ = kSlots * kSlot;       // 8 blocks x [64 heads][128 B]
 constexpr uint32_t kOffP = kOffQ + 65536;        // [64 keys][128 B]
 constexpr uint32_t kOffBar = kOffP + kBlk;
 constexpr uint32_t kOffMisc = kOffBar + 320;     // abort flag, TMEM address, the block's range
-constexpr uint32_t kOffRow = kOffMisc + 64;      // [4 tiles][64] row addresses, bit 0: FP8
+constexpr uint32_t kOffRow = kOffMisc + 128;      // [4 tiles][64] row addresses, bit 0: FP8
 constexpr uint32_t kOffRed = kOffRow + kAhead * kKT * 8;  // [4][64] floats
 constexpr uint32_t kOffMrun = kOffRed + 1024;
 constexpr uint32_t kOffAlpha = kOffMrun + 256;
@@ -192,7 +192,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  PagedWalk walk(*s_range);
+  PagedRange walk = *s_range;
   PagedSegment sg;
 
   if (warp < 8) {
@@ -342,10 +342,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
             lpart[2 * j + 1] *= al.y;
           }
         }
-        if (a.weights) {
-          if (st < kH) a.tile_ref[(int64_t)(sg.t + tile) * kH + st] = mrun[st];
-          if (st == 0) a.tile_of[sg.t + tile] = make_int2(sg.item, sg.tile0 + tile);
-        }
+        if (a.weights && st < kH) a.tile_ref[((int64_t)sg.item * a.item_tiles + sg.tile0 + tile) * kH + st] = mrun[st];
         uint32_t pa[4], pb[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -474,10 +471,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
       named_bar(1, 256);
     }
     if (!waited) pdl_wait();
-    if (st == 0) {
-      a.cut[blockIdx.x] = cut;
-      if (blockIdx.x == 0) *a.total = s_range->total;
-    }
+    if (st == 0) a.cut[blockIdx.x] = cut;
     if (st < kH) bulk_wait0();
   } else if (warp == kMmaWarp) {
     // =================== MMA issuer ===================
@@ -535,7 +529,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
         __syncwarp();
         tc_fence_after();
         if (a.weights && lane == 0) {  // P^T as it lies, for the weights
-          bulk_s2g(a.tile_p + (int64_t)(sg.t + tile) * kKT * kH, p_base, kKT * kH * 2);
+          bulk_s2g(a.tile_p + ((int64_t)sg.item * a.item_tiles + sg.tile0 + tile) * kKT * kH, p_base, kKT * kH * 2);
           bulk_commit();
         }
         __syncwarp();
@@ -599,42 +593,43 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
             cp_async_arrive(bar(kKVFull + u % kSlots));
           }
         } else {
-          // FP8 rows: a thread takes 16 dims of four rows; the codes of a chunk
-          // are loaded before its slot is waited for, expanded (code times
-          // the block's power of two, exact in bf16) and stored.  Rows of the
-          // window and the RoPE dims are bf16 and copied as they are.
+          // FP8 rows: a thread takes 16 dims of four rows.  A chunk's codes are
+          // loaded while the one before is expanded (code times the block's
+          // power of two, exact in bf16) and stored; rows of the window and
+          // the RoPE dims are bf16 and copied as they are.
           const int p8 = pt & 7;
-          for (int c = 0; c < 4; ++c) {
-            const uint32_t u = 4 * gt + c;
-            const bool codes = c < 3 || p8 < 4;
-            uint4 w0[4], w1[4];
-            uint32_t sc[4];
+          unsigned long long rv[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) rv[i] = rp[(pt >> 3) + 16 * i];
+          auto load = [&](int c, uint4 (&w0)[4], uint4 (&w1)[4], uint32_t (&sc)[4]) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              const unsigned long long v = rp[(pt >> 3) + 16 * i];
-              const uint8_t* src = reinterpret_cast<const uint8_t*>(v & ~1ull);
+              const uint8_t* src = reinterpret_cast<const uint8_t*>(rv[i] & ~1ull);
               w0[i] = w1[i] = make_uint4(0, 0, 0, 0);
               sc[i] = 0;
-              if (v & 1ull) {
-                if (codes) {
+              if (rv[i] & 1ull) {
+                if (c < 3 || p8 < 4) {
                   w0[i] = *reinterpret_cast<const uint4*>(src + c * 128 + p8 * 16);
-                  sc[i] = src[kD - a.R + 2 * a.R + 4 * c + (p8 >> 1)];
+                  sc[i] = src[kD + 64 + 4 * c + (p8 >> 1)];
                 } else {  // dims 448 + 16 (p8 - 4) ..
                   w0[i] = *reinterpret_cast<const uint4*>(src + 448 + (p8 - 4) * 32);
                   w1[i] = *reinterpret_cast<const uint4*>(src + 448 + (p8 - 4) * 32 + 16);
                 }
-              } else if (v) {
+              } else if (rv[i]) {
                 w0[i] = *reinterpret_cast<const uint4*>(src + c * 256 + p8 * 32);
                 w1[i] = *reinterpret_cast<const uint4*>(src + c * 256 + p8 * 32 + 16);
               }
             }
+          };
+          auto store = [&](int c, uint4 (&w0)[4], uint4 (&w1)[4], uint32_t (&sc)[4]) {
+            const uint32_t u = 4 * gt + c;
             acquire(u);
             const uint32_t blk = kv_base + (u % kSlots) * kSlot + (uint32_t)(p8 >> 2) * kBlk;
             const int q0 = (2 * p8) & 7;  // 16-byte piece of the 128-byte row
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const int row = (pt >> 3) + 16 * i;
-              if (codes && (rp[row] & 1ull)) {
+              if ((rv[i] & 1ull) && (c < 3 || p8 < 4)) {
                 const float s = mx_scale((int)sc[i]);
                 const uint32_t wd[4] = {w0[i].x, w0[i].y, w0[i].z, w0[i].w};
                 uint32_t o[8];
@@ -651,6 +646,16 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
             }
             fence_async_smem();
             mbar_arrive(bar(kKVFull + u % kSlots));
+          };
+          uint4 wa0[4], wa1[4], wb0[4], wb1[4];
+          uint32_t sa[4], sb[4];
+          load(0, wa0, wa1, sa);
+#pragma unroll 1
+          for (int c = 0; c < 4; c += 2) {
+            load(c + 1, wb0, wb1, sb);
+            store(c, wa0, wa1, sa);
+            if (c == 0) load(2, wa0, wa1, sa);
+            store(c + 1, wb0, wb1, sb);
           }
         }
         mbar_arrive(bar(kRowEmpty + rs));
@@ -694,7 +699,6 @@ void paged_shape_tc(PagedArgs* a) {
   a->hn = kH;
   a->kt = kKT;
   a->G = 148;
-  a->p_swizzled = 1;
 }
 
 cudaError_t launch_paged_attend_tc(const PagedArgs& a, cudaStream_t s) {
