@@ -702,7 +702,7 @@ int ds4a_quantize_mxfp4(int n_rows, int K, const ds4a_bf16* in, int64_t in_strid
   if (n_rows == 0) return DS4A_OK;
   if (!in || !codes || !scales || !aligned16(in) || !aligned16(codes) || !aligned16(scales)) return DS4A_EINVAL;
   if (in_stride < K || in_stride % 8 != 0) return DS4A_EINVAL;
-  return cuda_rc(launch_quantize_mxfp4(n_rows, K, in, false, in_stride, codes, scales, (cudaStream_t)stream));
+  return cuda_rc(launch_quantize_mxfp4(n_rows, K, in, in_stride, codes, scales, (cudaStream_t)stream));
 }
 
 static int check_oproj_mxfp4(const ds4a_oproj_cfg* c) {
@@ -712,13 +712,13 @@ static int check_oproj_mxfp4(const ds4a_oproj_cfg* c) {
   return DS4A_OK;
 }
 
-// quantised o, float intermediate, its quantised form
+// quantised o, quantised intermediate, partial sums of split products
 struct OprojMxfp4Ws {
   uint8_t *o_codes, *o_scales, *mid_codes, *mid_scales;
-  float* mid;
+  float* part;
 };
 static size_t oproj_mxfp4_layout(const ds4a_oproj_cfg* c, int M, void* ws, OprojMxfp4Ws* w) {
-  const int64_t k = (int64_t)c->n_heads * c->head_dim, n1 = (int64_t)c->n_groups * c->group_rank;
+  const int k = c->n_heads * c->head_dim, n1 = c->n_groups * c->group_rank;
   size_t at = 0;
   auto take = [&](size_t bytes) {
     unsigned char* p = ws ? static_cast<unsigned char*>(ws) + at : nullptr;
@@ -729,7 +729,9 @@ static size_t oproj_mxfp4_layout(const ds4a_oproj_cfg* c, int M, void* ws, Oproj
   w->o_scales = take((size_t)mxfp4_scale_bytes(M, k));
   w->mid_codes = take((size_t)M * n1 / 2);
   w->mid_scales = take((size_t)mxfp4_scale_bytes(M, n1));
-  w->mid = reinterpret_cast<float*>(take((size_t)M * n1 * 4));
+  const int s1 = mxfp4_ksplit(M, n1, k / c->n_groups), s2 = mxfp4_ksplit(M, c->hidden, n1);
+  const size_t p1 = s1 > 1 ? (size_t)s1 * M * n1 * 4 : 0, p2 = s2 > 1 ? (size_t)s2 * M * c->hidden * 4 : 0;
+  w->part = reinterpret_cast<float*>(take(p1 > p2 ? p1 : p2));
   return at;
 }
 
@@ -755,16 +757,15 @@ int ds4a_out_proj_mxfp4(const ds4a_oproj_cfg* cfg, int M, const ds4a_bf16* o, co
   cudaStream_t s = (cudaStream_t)stream;
   unsigned int* err = err_word();
   if (!err) return DS4A_ECUDA;
-  if (launch_quantize_mxfp4(M, k, o, false, k, w.o_codes, w.o_scales, s) != cudaSuccess) return DS4A_ECUDA;
+  if (launch_quantize_mxfp4(M, k, o, k, w.o_codes, w.o_scales, s) != cudaSuccess) return DS4A_ECUDA;
   Mxfp4Product p;
   p.M = M; p.N = n1; p.K = k1; p.n_per_group = cfg->group_rank; p.a_cols = k;
   p.a_codes = w.o_codes; p.a_scales = w.o_scales; p.b_codes = wa_codes; p.b_scales = wa_scales;
-  p.y = nullptr; p.mid = w.mid; p.err = err;
+  p.y = nullptr; p.q_codes = w.mid_codes; p.q_scales = w.mid_scales; p.part = w.part; p.err = err;
   if (launch_mxfp4_product(p, s) != cudaSuccess) return DS4A_ECUDA;
-  if (launch_quantize_mxfp4(M, n1, w.mid, true, n1, w.mid_codes, w.mid_scales, s) != cudaSuccess) return DS4A_ECUDA;
   p.N = cfg->hidden; p.K = n1; p.n_per_group = cfg->hidden; p.a_cols = n1;
   p.a_codes = w.mid_codes; p.a_scales = w.mid_scales; p.b_codes = wb_codes; p.b_scales = wb_scales;
-  p.y = y; p.mid = nullptr;
+  p.y = y; p.q_codes = p.q_scales = nullptr;
   return cuda_rc(launch_mxfp4_product(p, s));
 }
 

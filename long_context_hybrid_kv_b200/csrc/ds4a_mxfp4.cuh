@@ -21,21 +21,24 @@ __host__ __device__ constexpr int64_t mxfp4_scale_at(int64_t row, int64_t block,
   return ((row / 128) * (K / 128) + block / 4) * 512 + (row % 32) * 16 + (row % 128) / 32 * 4 + block % 4;
 }
 
-// bf16 (or, f32 set, float) rows -> codes and scales; padding rows of the
-// last block of 128 get zero scales
-cudaError_t launch_quantize_mxfp4(int n_rows, int K, const void* in, bool f32, int64_t in_stride, uint8_t* codes,
+// bf16 rows -> codes and scales; padding rows of the last block of 128 get
+// zero scales
+cudaError_t launch_quantize_mxfp4(int n_rows, int K, const uint16_t* in, int64_t in_stride, uint8_t* codes,
                                   uint8_t* scales, cudaStream_t s);
 
 // One grouped product: outputs n of group j = n / n_per_group take the
-// columns j * k .. (j + 1) * k of A's a_cols.  Either y (bf16 [M][N]) or mid
-// (float [M][N]) is written.
+// columns j * K .. (j + 1) * K of A's a_cols.  The result goes out as bf16
+// (y), or quantised again (q_codes, q_scales) for a next product over N.
+// part: float [mxfp4_ksplit][M][N] when the K axis is split.
 struct Mxfp4Product {
   int M, N, K, n_per_group, a_cols;
   const uint8_t *a_codes, *a_scales, *b_codes, *b_scales;
   uint16_t* y;
-  float* mid;
+  uint8_t *q_codes, *q_scales;
+  float* part;
   unsigned int* err;
 };
+int mxfp4_ksplit(int M, int N, int K);
 cudaError_t launch_mxfp4_product(const Mxfp4Product& p, cudaStream_t s);
 
 }  // namespace ds4a
