@@ -725,11 +725,16 @@ static size_t oproj_mxfp4_layout(const ds4a_oproj_cfg* c, int M, void* ws, Oproj
     at += (bytes + 255) / 256 * 256;
     return p;
   };
-  w->o_codes = take((size_t)M * k / 2);
-  w->o_scales = take((size_t)mxfp4_scale_bytes(M, k));
+  const int k1 = k / c->n_groups;
+  if (!mxfp4_small(M)) {
+    w->o_codes = take((size_t)M * k / 2);
+    w->o_scales = take((size_t)mxfp4_scale_bytes(M, k));
+  } else {
+    w->o_codes = w->o_scales = nullptr;
+  }
   w->mid_codes = take((size_t)M * n1 / 2);
   w->mid_scales = take((size_t)mxfp4_scale_bytes(M, n1));
-  const int s1 = mxfp4_ksplit(M, n1, k / c->n_groups), s2 = mxfp4_ksplit(M, c->hidden, n1);
+  const int s1 = mxfp4_small(M) ? 1 : mxfp4_ksplit(M, n1, k1), s2 = mxfp4_small(M) ? 1 : mxfp4_ksplit(M, c->hidden, n1);
   const size_t p1 = s1 > 1 ? (size_t)s1 * M * n1 * 4 : 0, p2 = s2 > 1 ? (size_t)s2 * M * c->hidden * 4 : 0;
   w->part = reinterpret_cast<float*>(take(p1 > p2 ? p1 : p2));
   return at;
@@ -757,12 +762,14 @@ int ds4a_out_proj_mxfp4(const ds4a_oproj_cfg* cfg, int M, const ds4a_bf16* o, co
   cudaStream_t s = (cudaStream_t)stream;
   unsigned int* err = err_word();
   if (!err) return DS4A_ECUDA;
-  if (launch_quantize_mxfp4(M, k, o, k, w.o_codes, w.o_scales, s) != cudaSuccess) return DS4A_ECUDA;
   Mxfp4Product p;
+  p.o = mxfp4_small(M) ? o : nullptr;  // few rows: the first product quantises them itself
+  if (!p.o && launch_quantize_mxfp4(M, k, o, k, w.o_codes, w.o_scales, s) != cudaSuccess) return DS4A_ECUDA;
   p.M = M; p.N = n1; p.K = k1; p.n_per_group = cfg->group_rank; p.a_cols = k;
   p.a_codes = w.o_codes; p.a_scales = w.o_scales; p.b_codes = wa_codes; p.b_scales = wa_scales;
   p.y = nullptr; p.q_codes = w.mid_codes; p.q_scales = w.mid_scales; p.part = w.part; p.err = err;
   if (launch_mxfp4_product(p, s) != cudaSuccess) return DS4A_ECUDA;
+  p.o = nullptr;
   p.N = cfg->hidden; p.K = n1; p.n_per_group = cfg->hidden; p.a_cols = n1;
   p.a_codes = w.mid_codes; p.a_scales = w.mid_scales; p.b_codes = wb_codes; p.b_scales = wb_scales;
   p.y = y; p.q_codes = p.q_scales = nullptr;

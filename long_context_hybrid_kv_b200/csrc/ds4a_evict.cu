@@ -10,9 +10,15 @@
 // leave, in order.  Sources and destinations are disjoint, every row moves at
 // most once, and one entry in, one entry out moves a single row.
 //
-// evict_select_kernel, one block per sequence: a radix select over the order-
-// preserving integer form of acc, then one ordered walk that ranks holes and
-// movers.  evict_move_kernel, over the whole GPU: the rows.
+// evict_keep_kernel, one block per sequence of up to 32768 slots, a thread up
+// to 32 slots in a row: the budget-th largest weight by bisection over its
+// order-preserving integer form, the keys in registers (a count of all of them
+// is a few instructions a key and one barrier, without the contention that a
+// histogram of weights, which share their exponents, has; it ends as soon as a
+// bound leaves exactly `budget`), then two scans rank holes and movers.
+// evict_select_kernel does the same by radix select from memory, for more
+// slots.  evict_move_kernel, over the whole GPU: the rows; few are moved by the
+// first kernel itself.
 #include "ds4a_evict.cuh"
 
 namespace ds4a {
@@ -102,12 +108,33 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictArgs 
       if ((k & mask) == prefix) atomicAdd(&hist[(k >> shift) & 255u], 1u);
     }
     __syncthreads();
-    if (tid == 0) {
-      unsigned int above = 0;
-      int d = 255;
-      while (d > 0 && above + hist[d] < need) above += hist[d--];
-      s_digit = (unsigned int)d;
-      s_above = above;
+    // the digit at which the keys from the top on reach `need`: lane l of
+    // the first warp sums the digits 255 - 8l .. 248 - 8l
+    if (tid < 32) {
+      unsigned int h[8], c = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        h[i] = hist[255 - 8 * tid - i];
+        c += h[i];
+      }
+      unsigned int up = c;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const unsigned int u = __shfl_up_sync(0xffffffffu, up, o);
+        if (tid >= o) up += u;
+      }
+      up -= c;  // above this lane's digits
+      if (up < need && up + c >= need) {
+        int i = 0;
+        while (up + h[0] < need) {
+          up += h[0];
+#pragma unroll
+          for (int q = 0; q < 7; ++q) h[q] = h[q + 1];
+          ++i;
+        }
+        s_digit = (unsigned int)(255 - 8 * tid - i);
+        s_above = up;
+      }
     }
     __syncthreads();
     prefix |= s_digit << shift;
@@ -156,42 +183,191 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictArgs 
   }
 }
 
-// rows in 16-byte pieces, a warp a row
+// row of a slot, or nullptr (a bad page)
+__device__ __forceinline__ uint8_t* evict_row(const EvictArgs& a, int b, int slot) {
+  const int pg = slot / a.page_size;
+  const int ph = a.table[(int64_t)b * a.table_stride + pg];
+  if (ph < 0 || ph >= a.n_pages) return nullptr;
+  return a.pages + ((int64_t)ph * a.page_size + (slot - pg * a.page_size)) * a.row_bytes;
+}
+// a warp moves a row, in 16-byte pieces
+__device__ __forceinline__ void evict_move_row(const EvictArgs& a, int b, int from, int to) {
+  const int lane = threadIdx.x & 31;
+  const uint8_t* src = evict_row(a, b, from);
+  uint8_t* dst = evict_row(a, b, to);
+  if (!src || !dst) {
+    if (lane == 0) raise_err(a.err, DS4A_DEV_BAD_INDEX);
+    return;
+  }
+  for (int i = lane * 16; i < a.row_bytes; i += 512)
+    *reinterpret_cast<uint4*>(dst + i) = *reinterpret_cast<const uint4*>(src + i);
+}
+
+// kPer slots a thread
+template <int kPer>
+__global__ void __launch_bounds__(kThreads, 1) evict_keep_kernel(const EvictArgs a, int move_here) {
+  extern __shared__ unsigned int keys[];  // slot s at s + s / 32 (a thread's run of 32 would be one bank)
+  __shared__ int2 sums[kThreads / 32];
+  __shared__ int counts[2][kThreads / 32];
+  const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  pdl_trigger();
+  pdl_wait();
+  const int pos = a.q_pos[b], gone = a.drop[b];
+  if (pos < 0) {
+    if (tid == 0) {
+      raise_err(a.err, DS4A_DEV_BAD_POS);
+      a.moves[b] = 0;
+    }
+    return;
+  }
+  const int closed = (int)(((unsigned)pos + 1u) / (unsigned)a.m);
+  const int n = max(0, min(closed - gone, a.cap)), budget = a.budget;
+  float* acc = a.acc + (int64_t)b * a.stride;
+  int32_t* entry = a.entry + (int64_t)b * a.stride;
+  const uint16_t* w = a.w ? a.w + (int64_t)b * a.w_stride : nullptr;
+  const bool full = n > budget;
+  const int oldest_kept = closed - a.recent;  // entries from here on are protected
+#pragma unroll 4
+  for (int s = tid; s < n; s += kThreads) {
+    float x = acc[s];
+    if (w) {
+      x += bf2f(w[s]);
+      acc[s] = x;
+    }
+    if (full) {
+      int e = entry[s];
+      if (e < 0) {
+        e = s + gone;
+        entry[s] = e;
+      }
+      keys[s + (s >> 5)] = evict_key(x, e >= oldest_kept);
+    }
+  }
+  if (!full) {
+    if (tid == 0) a.moves[b] = 0;
+    return;
+  }
+  __syncthreads();
+  const int s0 = tid * kPer;
+  unsigned int key[kPer];
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) key[i] = s0 + i < n ? keys[s0 + i + ((s0 + i) >> 5)] : 0u;
+  int round = 0;
+  auto count = [&](unsigned int bound) {  // keys >= bound (> 0), over the block
+    int c = 0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) c += key[i] >= bound;
+    c = __reduce_add_sync(0xffffffffu, c);
+    int* buf = counts[round++ & 1];
+    if (lane == 0) buf[warp] = c;
+    __syncthreads();
+    return __reduce_add_sync(0xffffffffu, buf[lane]);
+  };
+  // the largest bound that leaves `budget` keys or more; `above`: keys over it
+  unsigned int bound = 0;
+  int above = n;
+  bool exact = false;
+  for (int bit = 31; bit >= 0; --bit) {
+    const unsigned int b2 = bound | (1u << bit);
+    const int c = count(b2);
+    if (c >= budget) bound = b2;
+    else above = c;
+    if (c == budget) {
+      exact = true;
+      break;
+    }
+  }
+  // a key above the bound is kept, of the equal ones the lowest `need`
+  const int need = exact ? 0x7FFFFFFF : budget - (above == n ? 0 : above);
+  int2 total;
+  int ties = 0;
+  if (!exact) {
+    int mine = 0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) mine += s0 + i < n && key[i] == bound;
+    ties = block_scan(mine, 0, sums, &total).x;
+  }
+  unsigned int keep = 0;
+  int holes = 0, movers = 0;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int s = s0 + i;
+    if (s >= n) break;
+    const bool k = key[i] > bound || (key[i] == bound && ties++ < need);
+    keep |= (k ? 1u : 0u) << i;
+    holes += s < budget && !k;
+    movers += s >= budget && k;
+  }
+  int2 at = block_scan(holes, movers, sums, &total);
+  int32_t* dst = a.list + (int64_t)b * 2 * budget;
+  int32_t* src = dst + budget;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int s = s0 + i;
+    if (s >= n) break;
+    const bool k = keep >> i & 1u;
+    if (s < budget && !k) dst[at.x++] = s;
+    if (s >= budget && k) src[at.y++] = s;
+  }
+  __syncthreads();
+  const int moved = total.y;
+  for (int r = tid; r < moved; r += kThreads) {
+    const int from = src[r], to = dst[r];
+    acc[to] = acc[from];
+    entry[to] = entry[from];
+  }
+  if (move_here)
+    for (int r = warp; r < moved; r += kThreads / 32) evict_move_row(a, b, src[r], dst[r]);
+  __syncthreads();
+  // slots behind the kept ones start over
+  for (int s = budget + tid; s < a.cap; s += kThreads) {
+    acc[s] = 0.f;
+    entry[s] = -1;
+  }
+  if (tid == 0) {
+    a.moves[b] = moved;
+    a.drop[b] = gone + (n - budget);
+  }
+}
+
 __global__ void __launch_bounds__(256) evict_move_kernel(const EvictArgs a) {
-  const int b = blockIdx.y, lane = threadIdx.x & 31;
+  const int b = blockIdx.y;
   pdl_trigger();
   pdl_wait();
   const int moves = a.moves[b];
   const int32_t* dst = a.list + (int64_t)b * 2 * a.budget;
   const int32_t* src = dst + a.budget;
-  auto row = [&](int slot) -> uint8_t* {
-    const int pg = slot / a.page_size;
-    const int ph = a.table[(int64_t)b * a.table_stride + pg];
-    if (ph < 0 || ph >= a.n_pages) return nullptr;
-    return a.pages + ((int64_t)ph * a.page_size + (slot - pg * a.page_size)) * a.row_bytes;
-  };
-  for (int r = blockIdx.x * 8 + (threadIdx.x >> 5); r < moves; r += gridDim.x * 8) {
-    uint8_t* to = row(dst[r]);
-    const uint8_t* from = row(src[r]);
-    if (!to || !from) {
-      if (lane == 0) raise_err(a.err, DS4A_DEV_BAD_INDEX);
-      continue;
-    }
-    for (int i = lane * 16; i < a.row_bytes; i += 512)
-      *reinterpret_cast<uint4*>(to + i) = *reinterpret_cast<const uint4*>(from + i);
-  }
+  for (int r = blockIdx.x * 8 + (threadIdx.x >> 5); r < moves; r += gridDim.x * 8) evict_move_row(a, b, src[r], dst[r]);
+}
+
+template <int kPer>
+cudaError_t launch_keep(const EvictArgs& a, int move_here, cudaStream_t s) {
+  const int slots = kPer * kThreads, smem = (slots + slots / 32) * 4;
+  static std::atomic<int> cache[kMaxDevices];
+  const cudaError_t e = ensure_smem(evict_keep_kernel<kPer>, smem, cache);
+  if (e != cudaSuccess) return e;
+  TraceScope tr("evict_keep", s);
+  return launch_pdl(evict_keep_kernel<kPer>, dim3(a.B), dim3(kThreads), smem, s, a, move_here);
 }
 
 }  // namespace
 
 cudaError_t launch_evict(const EvictArgs& a, cudaStream_t s) {
-  {
+  const int most = min(a.budget, a.cap - a.budget);  // rows that a sequence may move
+  const int move_here = most <= 64;                  // two rows a warp: less than a launch
+  const int per = (a.cap + kThreads - 1) / kThreads;
+  cudaError_t e;
+  if (per <= 1) e = launch_keep<1>(a, move_here, s);
+  else if (per <= 4) e = launch_keep<4>(a, move_here, s);
+  else if (per <= 8) e = launch_keep<8>(a, move_here, s);
+  else if (per <= 16) e = launch_keep<16>(a, move_here, s);
+  else if (per <= 32) e = launch_keep<32>(a, move_here, s);
+  else {
     TraceScope tr("evict_select", s);
-    const cudaError_t e = launch_pdl(evict_select_kernel, dim3(a.B), dim3(kThreads), 0, s, a);
-    if (e != cudaSuccess) return e;
+    e = launch_pdl(evict_select_kernel, dim3(a.B), dim3(kThreads), 0, s, a);
   }
+  if (e != cudaSuccess || (move_here && per <= 32)) return e;
   TraceScope tr("evict_move", s);
-  const int most = min(a.budget, a.cap - a.budget);
   const int blocks = max(1, min((most + 7) / 8, 148 * 8 / a.B));
   return launch_pdl(evict_move_kernel, dim3(blocks, a.B), dim3(256), 0, s, a);
 }

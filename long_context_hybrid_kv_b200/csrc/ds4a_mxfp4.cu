@@ -51,42 +51,58 @@ __device__ __forceinline__ int mx_block(const float (&v)[32], uint4* codes) {
   return code;
 }
 
-// A thread a 32-value block.  64 bytes in, 16.5 out: bound by HBM.
+// the same for 32 bf16 values: the largest magnitude as 16-bit integers, two at
+// a time (positive floats order like their bits)
+__device__ __forceinline__ int mx_block_words(const uint4 (&u)[4], uint4* codes) {
+  unsigned int m = 0;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    m = __vmaxu2(m, u[q].x & 0x7FFF7FFFu);
+    m = __vmaxu2(m, u[q].y & 0x7FFF7FFFu);
+    m = __vmaxu2(m, u[q].z & 0x7FFF7FFFu);
+    m = __vmaxu2(m, u[q].w & 0x7FFF7FFFu);
+  }
+  m = max(m & 0xFFFFu, m >> 16);
+  const int code = mx_scale_code<true>(__uint_as_float(m << 16));
+  const float inv = mx_inv_scale(code);
+  const float2 inv2 = make_float2(inv, inv);
+  uint32_t w[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const unsigned int x[4] = {u[q].x, u[q].y, u[q].z, u[q].w};
+    w[q] = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float2 f = mul_f2(bf2x2_to_f2(x[k]), inv2);
+      w[q] |= to_e2m1x2(f.x, f.y) << (8 * k);
+    }
+  }
+  *codes = make_uint4(w[0], w[1], w[2], w[3]);
+  return code;
+}
+
+// A thread a 32-value block.  64 bytes in, 16.5 out: bound by HBM (16384 x
+// 32768 values in 223 us, 6.1 TB/s).
 __global__ void __launch_bounds__(256) quantize_mxfp4_kernel(int n_rows, int rows_pad, int K, const uint16_t* in,
                                                              int64_t in_stride, uint8_t* codes, uint8_t* scales) {
   pdl_trigger();
+  pdl_wait();
   const int kb = K / kMxBlock;
   const int64_t n = (int64_t)rows_pad * kb;
-  bool waited = false;
   for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < n; i += (int64_t)gridDim.x * blockDim.x) {
     const int64_t row = i / kb;
     const int blk = (int)(i - row * kb);
     int code = 0;
     uint4 c = make_uint4(0, 0, 0, 0);
     if (row < n_rows) {
-      const uint4* p = reinterpret_cast<const uint4*>(in + row * in_stride + blk * kMxBlock);
       uint4 u[4];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) u[q] = p[q];
-      float v[32];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const unsigned int x[4] = {u[q].x, u[q].y, u[q].z, u[q].w};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float2 f = bf2x2_to_f2(x[k]);
-          v[8 * q + 2 * k] = f.x;
-          v[8 * q + 2 * k + 1] = f.y;
-        }
-      }
-      code = mx_block(v, &c);
+      for (int q = 0; q < 4; ++q) u[q] = reinterpret_cast<const uint4*>(in + row * in_stride + blk * kMxBlock)[q];
+      code = mx_block_words(u, &c);
     }
-    if (!waited) pdl_wait();  // (the rows are an input; what is written may still be read)
-    waited = true;
     if (row < n_rows) *reinterpret_cast<uint4*>(codes + row * (K / 2) + blk * 16) = c;
     scales[mxfp4_scale_at(row, blk, K)] = (uint8_t)code;
   }
-  if (!waited) pdl_wait();
 }
 
 constexpr int kBM = 128, kBN = 256, kBK = 256;
@@ -398,6 +414,240 @@ __global__ void __launch_bounds__(128) mxfp4_finish_kernel(const GemmParams p) {
   }
 }
 
+// ---------------------------------------------------------------------------
+// Up to 128 rows (a decode batch): the weights stream past once, and what
+// counts is the chain of latencies.  K is split over a cluster of up to four
+// blocks (a cluster of eight waited for room: 23 us instead of 15 for the
+// second product), tiles are 256 or 128 outputs wide, whichever fills the SMs
+// better, and a block's ring holds half of its loads or all of them, the
+// weights' out before the kernel ahead has ended.  The first product quantises
+// its rows of o straight into the operand (a 32-value block is one 16-byte
+// piece of the swizzled row), four warps a stage, so no kernel does it
+// before.  The blocks of a cluster leave their float sums in shared memory and
+// each adds a share of the columns, in the order of the splits, and finishes
+// it: two launches in all instead of five.
+// ---------------------------------------------------------------------------
+constexpr int kQuantWarps = 16;  // that quantise; the first four of them read the sums
+constexpr int kSmallThreads = 64 + 32 * kQuantWarps;
+template <int kN>
+struct Small {  // a tile kN outputs wide
+  static constexpr int kRing = kN == 256 ? 4 : 6;
+  static constexpr uint32_t kB = kN * kBK / 2, kSA = kStageA + kB, kSB = kSA + 1024, kStage = kSB + kN * 8;
+  static constexpr uint32_t kBar = kRing * kStage, kMisc = kBar + 256, kBytes = kMisc + 64 + 1024;
+  static constexpr uint32_t kPitch = kN * 4 + 16;  // bytes of a row of sums: rows fall into different banks
+  static_assert(kStage % 1024 == 0 && kBytes <= 232448 && 128 * kPitch <= kBar, "shared memory");
+};
+
+__device__ __forceinline__ float4 ld_cluster4(uint32_t addr, uint32_t rank) {
+  uint32_t at;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(addr), "r"(rank));
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at) : "memory");
+  return v;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// kQuant: A is quantised from o (bf16 [M][o_cols]) here; kMx: the result goes
+// out quantised, else as bf16
+template <int kN, bool kQuant, bool kMx>
+__global__ void __launch_bounds__(kSmallThreads, 1)
+    mxfp4_small_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap,
+                       const __grid_constant__ GemmParams p, const uint16_t* __restrict__ o, int64_t o_cols) {
+  using S = Small<kN>;
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  unsigned char* smem =
+      reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  const uint32_t sbase = smem_u32(smem);
+  auto full = [&](int j) { return sbase + S::kBar + 8u * (uint32_t)(j % S::kRing); };
+  auto empty = [&](int j) { return sbase + S::kBar + 64u + 8u * (uint32_t)(j % S::kRing); };
+  const uint32_t acc_full = sbase + S::kBar + 128u;
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + S::kMisc);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + S::kMisc + 8);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  unsigned int* err = p.err;
+  // the blocks of a cluster are the splits of one tile
+  const int split = blockIdx.x % p.ksplit, n0 = blockIdx.x / p.ksplit * kN;
+  const int k0 = split * p.steps_per_split, steps = max(0, min(p.k_steps, k0 + p.steps_per_split) - k0);
+  const int a_blk = n0 / p.n_per_group * p.a_group_blocks;
+
+  pdl_trigger();
+  if (tid == 0) {
+    *abort_flag = 0;
+    for (int j = 0; j < S::kRing; ++j) {
+      mbar_init(full(j), kQuant ? 8 * kQuantWarps + 1 : 1);
+      mbar_init(empty(j), 1);
+    }
+    mbar_init(acc_full, 1);
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_slot), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      auto load_b = [&](int j) {
+        const uint32_t dst = sbase + (j % S::kRing) * S::kStage;
+        mbar_expect_tx(full(j), S::kB + kN * 8u + (kQuant ? 0u : kStageA + 1024u));
+        tma_load_2d(dst + kStageA, &bmap, (k0 + j) * (kBK / 2), n0, full(j));
+        const uint8_t* sb = p.b_scales + ((int64_t)(n0 / 128) * p.b_blocks + 2 * (k0 + j)) * 512;
+        bulk_g2s(dst + S::kSB, sb, 1024, full(j));
+        if (kN == 256) bulk_g2s(dst + S::kSB + 1024, sb + p.b_blocks * 512, 1024, full(j));
+      };
+      auto load_a = [&](int j) {
+        if (kQuant) return;
+        const uint32_t dst = sbase + (j % S::kRing) * S::kStage;
+        tma_load_2d(dst, &amap, (a_blk + 2 * (k0 + j)) * 64, 0, full(j));
+        bulk_g2s(dst + S::kSA, p.a_scales + ((int64_t)a_blk + 2 * (k0 + j)) * 512, 1024, full(j));
+      };
+      const int first = min(steps, S::kRing);
+      for (int j = 0; j < first; ++j) load_b(j);
+      pdl_wait();
+      for (int j = 0; j < first; ++j) load_a(j);
+      int sent = first;
+      for (; sent < steps; ++sent) {
+        if (!mbar_wait(empty(sent), (sent / S::kRing - 1) & 1u, abort_flag, err)) break;
+        load_b(sent);
+        load_a(sent);
+      }
+      for (int j = max(0, sent - S::kRing); j < sent; ++j) mbar_drain(full(j), (j / S::kRing) & 1u);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    for (int j = 0; j < steps; ++j) {
+      const uint32_t st = sbase + (j % S::kRing) * S::kStage;
+      mbar_wait(full(j), (j / S::kRing) & 1u, abort_flag, err);
+      __syncwarp();
+      tc_fence_after();
+      const uint64_t sa = sdesc_scales(st + S::kSA), sb = sdesc_scales(st + S::kSB);
+#pragma unroll
+      for (uint32_t i = 0; i < 2; ++i) {
+        scales_to_tmem_elect(tmem + kColSA + 4 * i, sa + ((512u * i) >> 4));
+        scales_to_tmem_elect(tmem + kColSB + 8 * i, sb + ((512u * i) >> 4));
+        if (kN == 256) scales_to_tmem_elect(tmem + kColSB + 8 * i + 4, sb + ((1024u + 512u * i) >> 4));
+      }
+      const uint64_t da = sdesc_sw128(st, 16, 1024), db = sdesc_sw128(st + kStageA, 16, 1024);
+#pragma unroll
+      for (uint32_t i = 0; i < 4; ++i)
+        mma_mxf4_elect(tmem, da + ((32u * i) >> 4), db + ((32u * i) >> 4), idesc_mxf4(kBM, kN, 2 * (i & 1)),
+                       tmem + kColSA + 4 * (i >> 1), tmem + kColSB + 8 * (i >> 1), j > 0 || i > 0 ? 1u : 0u);
+      commit_elect(empty(j));
+    }
+    commit_elect(acc_full);
+    mbar_wait(acc_full, 0, abort_flag, err);  // every MMA has finished before the block exits
+    __syncwarp();
+  } else {
+    pdl_wait();
+    if (kQuant) {
+      // warps 2 + q, 6 + q, ... quantise the steps q, q + 4, ...  (Rows behind the
+      // last are left as they are: whatever lies there only reaches rows of
+      // the sums that are not looked at.)
+      const int t = (warp - 2) / 4 * 32 + lane;
+      constexpr int kT = 8 * kQuantWarps;
+      for (int j = (warp - 2) & 3; j < steps; j += 4) {
+        if (j >= S::kRing) mbar_wait(empty(j), (j / S::kRing - 1) & 1u, abort_flag, err);
+        unsigned char* st = smem + (j % S::kRing) * S::kStage;
+        const uint16_t* src = o + ((int64_t)a_blk + 2 * (k0 + j)) * 128;
+        for (int i0 = t; i0 < p.M * 8; i0 += 4 * kT) {
+          uint4 u[4][4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int i = min(i0 + kT * q, p.M * 8 - 1);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) u[q][c] = reinterpret_cast<const uint4*>(src + (i >> 3) * o_cols + (i & 7) * 32)[c];
+          }
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int i = i0 + kT * q, row = i >> 3, blk = i & 7;
+            if (i >= p.M * 8) break;
+            uint4 codes;
+            const int code = mx_block_words(u[q], &codes);
+            *reinterpret_cast<uint4*>(st + sw128((uint32_t)row, (uint32_t)blk)) = codes;
+            st[S::kSA + (blk >> 2) * 512 + (row & 31) * 16 + (row >> 5) * 4 + (blk & 3)] = (unsigned char)code;
+          }
+        }
+        fence_async_smem();
+        mbar_arrive(full(j));
+      }
+    }
+    if (warp < 6) {
+      // the sums of this split into shared memory (the ring has been read)
+      const int quarter = warp & 3, r = quarter * 32 + lane;
+      mbar_wait(acc_full, 0, abort_flag, err);
+      __syncwarp();
+      tc_fence_after();
+      if (quarter * 32 < p.M) {
+        const uint32_t t_lane = tmem + ((uint32_t)(quarter * 32) << 16);
+#pragma unroll 1
+        for (int c = 0; c < kN / 32; c += 2) {
+          float v[32], x[32];
+          tmem_ld32(t_lane + (uint32_t)(c * 32), v);
+          tmem_ld32(t_lane + (uint32_t)(c * 32 + 32), x);
+          tmem_ld_wait();
+          if (r < p.M) {
+            float4* dst = reinterpret_cast<float4*>(smem + r * S::kPitch + c * 128);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) dst[q] = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) dst[8 + q] = make_float4(x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]);
+          }
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem, 512);
+  pdl_wait();
+  if (p.ksplit > 1) cluster_sync();
+  // this block's columns of the tile: eight threads a 32-column block
+  const int cols = kN / p.ksplit, c_base = split * cols, per = cols / 4;  // threads a row
+  const int used = (p.k_steps + p.steps_per_split - 1) / p.steps_per_split;  // splits with steps
+  // (of the operand's padding rows neither codes nor scales are written: they
+  // only reach padding rows of the next sums)
+  for (int i = tid; i < p.M * per; i += kSmallThreads) {
+    const int row = i / per, c = c_base + (i - row * per) * 4, col = n0 + c;
+    const uint32_t at = (uint32_t)row * S::kPitch + (uint32_t)c * 4u;
+    float4 y[4];
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      y[s] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (s < used) y[s] = p.ksplit > 1 ? ld_cluster4(sbase + at, (uint32_t)s) : *reinterpret_cast<const float4*>(smem + at);
+    }
+    float4 x = y[0];
+#pragma unroll
+    for (int s = 1; s < 4; ++s) {
+      x.x += y[s].x;
+      x.y += y[s].y;
+      x.z += y[s].z;
+      x.w += y[s].w;
+    }
+    if (!kMx) {
+      *reinterpret_cast<uint2*>(p.y + (int64_t)row * p.N + col) = make_uint2(f2_to_bf2x2(x.x, x.y), f2_to_bf2x2(x.z, x.w));
+    } else {
+      // (M per is a multiple of eight: all threads of a block are here)
+      const unsigned int eight = 0xFFu << (lane & 24);
+      float amax = fmaxf(fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(x.z), fabsf(x.w)));
+#pragma unroll
+      for (int q = 1; q < 8; q <<= 1) amax = fmaxf(amax, __shfl_xor_sync(eight, amax, q));
+      const int code = mx_scale_code<true>(amax);
+      const float inv = mx_inv_scale(code);
+      const uint32_t two = to_e2m1x2(x.x * inv, x.y * inv) | (to_e2m1x2(x.z * inv, x.w * inv) << 8);
+      *reinterpret_cast<uint16_t*>(p.q_codes + (int64_t)row * (p.N / 2) + col / 2) = (uint16_t)two;
+      if ((tid & 7) == 0) p.q_scales[mxfp4_scale_at(row, col / 32, p.N)] = (uint8_t)code;
+    }
+  }
+  if (p.ksplit > 1) cluster_sync();  // no block leaves while another may still read its sums
+}
+
 // codes as rows of bytes, boxes of 128 bytes x box_rows
 bool encode_codes(CUtensorMap* map, const void* base, uint64_t row_bytes, uint64_t rows, uint32_t box_rows) {
   PFN_cuTensorMapEncodeTiled_v12000 encode = get_encode();
@@ -440,21 +690,63 @@ int mxfp4_ksplit(int M, int N, int K) {
   return ks;
 }
 
-cudaError_t launch_mxfp4_product(const Mxfp4Product& q, cudaStream_t s) {
+bool mxfp4_small(int M) { return M <= kBM; }
+
+template <int kN, bool kQuant, bool kMx>
+static cudaError_t launch_small_kernel(const CUtensorMap& amap, const CUtensorMap& bmap, const GemmParams& p,
+                                       const uint16_t* o, int64_t o_cols, cudaStream_t s) {
+  static std::atomic<int> cache[kMaxDevices];
+  const cudaError_t e = ensure_smem(mxfp4_small_kernel<kN, kQuant, kMx>, (int)Small<kN>::kBytes, cache);
+  if (e != cudaSuccess) return e;
+  TraceScope tr("mxfp4_small", s);
+  return launch_pdl_cluster(mxfp4_small_kernel<kN, kQuant, kMx>, dim3(p.N / kN * p.ksplit), dim3(kSmallThreads),
+                            Small<kN>::kBytes, s, p.ksplit, amap, bmap, p, o, o_cols);
+}
+
+// The tile and the split of K (1, 2 or 4) that use most SMs, the wider tile
+// if both use as many: it quantises, or loads, A half as often.
+static cudaError_t launch_small(const Mxfp4Product& q, GemmParams p, cudaStream_t s) {
+  int best = 0, wide = 1;
+  p.ksplit = 1;
+  for (int w = 1; w >= 0; --w)
+    for (int ks = 1; ks <= 4; ks *= 2) {
+      const int blocks = q.N / (w ? 256 : 128) * ks;
+      if (ks > p.k_steps || (blocks > 148 && best > 0) || blocks <= best) continue;
+      best = blocks;
+      wide = w;
+      p.ksplit = ks;
+    }
+  p.steps_per_split = (p.k_steps + p.ksplit - 1) / p.ksplit;
   CUtensorMap amap, bmap;
-  if (!encode_codes(&amap, q.a_codes, (uint64_t)q.a_cols / 2, (uint64_t)q.M, kBM)) return cudaErrorInvalidValue;
-  if (!encode_codes(&bmap, q.b_codes, (uint64_t)q.K / 2, (uint64_t)q.N, kBN)) return cudaErrorInvalidValue;
+  memset(&amap, 0, sizeof(amap));
+  if (!q.o && !encode_codes(&amap, q.a_codes, (uint64_t)q.a_cols / 2, (uint64_t)q.M, kBM)) return cudaErrorInvalidValue;
+  if (!encode_codes(&bmap, q.b_codes, (uint64_t)q.K / 2, (uint64_t)q.N, wide ? 256 : 128)) return cudaErrorInvalidValue;
+#define DS4A_SMALL(n, quant, mx) launch_small_kernel<n, quant, mx>(amap, bmap, p, q.o, q.a_cols, s)
+  if (wide) {
+    if (q.o) return q.y ? DS4A_SMALL(256, true, false) : DS4A_SMALL(256, true, true);
+    return q.y ? DS4A_SMALL(256, false, false) : DS4A_SMALL(256, false, true);
+  }
+  if (q.o) return q.y ? DS4A_SMALL(128, true, false) : DS4A_SMALL(128, true, true);
+  return q.y ? DS4A_SMALL(128, false, false) : DS4A_SMALL(128, false, true);
+#undef DS4A_SMALL
+}
+
+cudaError_t launch_mxfp4_product(const Mxfp4Product& q, cudaStream_t s) {
   GemmParams p;
   p.M = q.M; p.N = q.N; p.k_steps = q.K / kBK; p.n_per_group = q.n_per_group;
   p.a_blocks = q.a_cols / 128; p.b_blocks = q.K / 128;
   p.a_group_blocks = q.n_per_group < q.N ? q.K / 128 : 0;
+  p.a_scales = q.a_scales; p.b_scales = q.b_scales;
+  p.y = q.y; p.q_codes = q.q_codes; p.q_scales = q.q_scales; p.part = q.part; p.err = q.err;
   p.m_tiles = (q.M + kBM - 1) / kBM; p.n_tiles = q.N / kBN;
+  if (mxfp4_small(q.M)) return launch_small(q, p, s);
+  CUtensorMap amap, bmap;
+  if (!encode_codes(&amap, q.a_codes, (uint64_t)q.a_cols / 2, (uint64_t)q.M, kBM)) return cudaErrorInvalidValue;
+  if (!encode_codes(&bmap, q.b_codes, (uint64_t)q.K / 2, (uint64_t)q.N, kBN)) return cudaErrorInvalidValue;
   p.ksplit = mxfp4_ksplit(q.M, q.N, q.K);
   p.steps_per_split = (p.k_steps + p.ksplit - 1) / p.ksplit;
   p.ksplit = (p.k_steps + p.steps_per_split - 1) / p.steps_per_split;  // no empty split
   p.n_units = p.m_tiles * p.n_tiles * p.ksplit;
-  p.a_scales = q.a_scales; p.b_scales = q.b_scales;
-  p.y = q.y; p.q_codes = q.q_codes; p.q_scales = q.q_scales; p.part = q.part; p.err = q.err;
   if (p.ksplit == 1)
     return q.y ? launch_gemm_kernel<kOutBf16>(amap, bmap, p, s) : launch_gemm_kernel<kOutMx>(amap, bmap, p, s);
   const cudaError_t e = launch_gemm_kernel<kOutPart>(amap, bmap, p, s);

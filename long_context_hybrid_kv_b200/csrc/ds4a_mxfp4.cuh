@@ -29,9 +29,11 @@ cudaError_t launch_quantize_mxfp4(int n_rows, int K, const uint16_t* in, int64_t
 // One grouped product: outputs n of group j = n / n_per_group take the
 // columns j * K .. (j + 1) * K of A's a_cols.  The result goes out as bf16
 // (y), or quantised again (q_codes, q_scales) for a next product over N.
-// part: float [mxfp4_ksplit][M][N] when the K axis is split.
+// part: float [mxfp4_ksplit][M][N] when the K axis is split.  o: A as bf16 [M]
+// [a_cols] instead of codes and scales, where mxfp4_small(M).
 struct Mxfp4Product {
   int M, N, K, n_per_group, a_cols;
+  const uint16_t* o;
   const uint8_t *a_codes, *a_scales, *b_codes, *b_scales;
   uint16_t* y;
   uint8_t *q_codes, *q_scales;
@@ -39,6 +41,7 @@ struct Mxfp4Product {
   unsigned int* err;
 };
 int mxfp4_ksplit(int M, int N, int K);
+bool mxfp4_small(int M);
 cudaError_t launch_mxfp4_product(const Mxfp4Product& p, cudaStream_t s);
 
 }  // namespace ds4a
