@@ -12,18 +12,18 @@
 // next to the 64 KiB of q^, so that the next tile is there and its first
 // product runs during this tile's softmax.
 //
-// Thread block (one per SM, 480 threads):
+// Thread block (one per SM, 608 threads):
 //   warps 0-7    q^ of every segment, softmax, epilogue: two warps per TMEM
 //                lane quarter with 32 heads each.  S^T of M = 64 has 16 keys
 //                in each quarter; a thread holds two keys x 8 heads of it, and
 //                later a dim row of O^T.
 //   warp 8       TMEM allocation; lane 0 issues the MMAs.
-//   warps 9-12   gather the rows by cp.async, a chunk (16 KiB) at a time, into
-//                a ring of nine, in the 128-byte swizzle.  FP8 rows go through
-//                registers and are expanded on the way.
-//   warps 13-14  one key a thread, up to four tiles ahead: index, page, row
+//   warps 9-10   one key a thread, up to four tiles ahead: index, page, row
 //                address, and a prefetch of the row into L2, so that HBM keeps
 //                streaming while the ring is full.
+//   warps 11-18  gather the rows by cp.async, a chunk (16 KiB) at a time, into
+//                a ring of nine, in the 128-byte swizzle.  FP8 rows go through
+//                registers, a tile ahead, and are expanded on the way.
 #include "ds4a_paged.cuh"
 #include "ds4a_tc.cuh"
 
@@ -34,10 +34,11 @@ using namespace tc;
 
 constexpr int kH = 64, kD = 512;
 constexpr int kKT = 64;               // keys per tile
-constexpr int kThreads = 480;
+constexpr int kThreads = 608;
 constexpr int kMmaWarp = 8;
-constexpr int kPG0 = 288;             // first gathering thread (warps 9-12)
-constexpr int kPtr0 = 416;            // first address thread (warps 13-14)
+constexpr int kPtr0 = 288;            // first address thread (warps 9-10)
+constexpr int kPG0 = 352;             // first gathering thread (warps 11-18)
+constexpr int kGather = kThreads - kPG0;
 constexpr int kSlots = 9;             // ring of 128-dim chunks
 constexpr int kAhead = 4;             // tiles of row addresses
 constexpr float kLog2e = 1.4426950408889634f;
@@ -64,7 +65,7 @@ static_assert(kSmemBytes <= 232448, "shared memory of a block");
 // bytes 1088 apart (the two heads that a warp writes at a time then lie in
 // different banks).
 constexpr uint32_t kStagePitch = 1088;
-static_assert(kH * kStagePitch <= 65536 + kBlk, "output stage");
+static_assert(kH * kStagePitch <= 65536 + kBlk && kH * kD * 4 <= kSlots * kSlot, "output stages");
 
 enum Bar {
   kKVFull = 0, kKVEmpty = kKVFull + kSlots, kRowFull = kKVEmpty + kSlots, kRowEmpty = kRowFull + kAhead,
@@ -160,12 +161,12 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
   if (tid == 0) {
     *abort_flag = 0;
     for (int i = 0; i < kSlots; ++i) {
-      mbar_init(bar(kKVFull + i), 128);
+      mbar_init(bar(kKVFull + i), kGather);
       mbar_init(bar(kKVEmpty + i), 1);
     }
     for (int i = 0; i < kAhead; ++i) {
       mbar_init(bar(kRowFull + i), kKT);
-      mbar_init(bar(kRowEmpty + i), 128 + kKT);  // the gatherers, and 64 softmax threads for all
+      mbar_init(bar(kRowEmpty + i), kGather + 64);  // the gatherers, and 64 softmax threads for all
     }
     mbar_init(bar(kQFull), 256);
     mbar_init(bar(kSFull0), 1);
@@ -215,20 +216,21 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
       // q^ = RoPE_pos(RMSNorm(q) g), rounded to bf16 (the MMA's operand), into
       // the K-major operand layout: warp w takes heads w, w + 8, ..., lane l
       // dims 8l .. 8l+7 and 256+8l ..; heads that the group does not have are
-      // 0.  All loads go out first.
-      uint4 va[8], vb[8];
-      {
+      // 0.  Four heads' loads at a time.
+      uint4 va[4], vb[4];
+      auto load_q = [&](int half) {
         const uint16_t* qrow = a.q + head0 * kD + 8 * lane;
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          const int h = warp + 8 * u;
+        for (int u = 0; u < 4; ++u) {
+          const int h = warp + 8 * (4 * half + u);
           va[u] = vb[u] = make_uint4(0, 0, 0, 0);
           if (h < nh) {
             va[u] = *reinterpret_cast<const uint4*>(qrow + h * kD);
             vb[u] = *reinterpret_cast<const uint4*>(qrow + h * kD + 256);
           }
         }
-      }
+      };
+      load_q(0);
       if (st < R / 2) {
         float cs, sn;
         rope_cos_sin(sg.seq.pos, a.rope.t[st], &cs, &sn);
@@ -249,32 +251,36 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
           rope[k] = d >= 0 ? rope_s[d >> 1] : make_float2(1.f, 0.f);
         }
         const uint32_t offA = (uint32_t)(lane >> 3) * 8192u, offB = (uint32_t)(4 + (lane >> 3)) * 8192u;
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half) {
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          const int h = warp + 8 * u;
-          const unsigned int wv[8] = {va[u].x, va[u].y, va[u].z, va[u].w, vb[u].x, vb[u].y, vb[u].z, vb[u].w};
-          float2 acc = make_float2(0.f, 0.f);
+          for (int u = 0; u < 4; ++u) {
+            const int h = warp + 8 * (4 * half + u);
+            const unsigned int wv[8] = {va[u].x, va[u].y, va[u].z, va[u].w, vb[u].x, vb[u].y, vb[u].z, vb[u].w};
+            float2 acc = make_float2(0.f, 0.f);
 #pragma unroll
-          for (int q = 0; q < 8; ++q) {
-            const float2 f = bf2x2_to_f2(wv[q]);
-            acc = fma_f2(f, f, acc);
-          }
-          // (a head that is not there: 0 rather than 0 / sqrt(eps))
-          const float ss = warp_sum(acc.x + acc.y);
-          const float rstd = h < nh ? rsqrtf(ss * (1.f / kD) + a.eps) : 0.f;
-          uint32_t pq[8];
-#pragma unroll
-          for (int q = 0; q < 8; ++q) {
-            float2 x = mul_f2(mul_f2(bf2x2_to_f2(wv[q]), make_float2(rstd, rstd)), g[q]);
-            if (q >= 4) {
-              const float2 cs = rope[q - 4];
-              x = fma_f2(make_float2(x.x, x.x), cs, mul_f2(make_float2(x.y, x.y), make_float2(-cs.y, cs.x)));
+            for (int q = 0; q < 8; ++q) {
+              const float2 f = bf2x2_to_f2(wv[q]);
+              acc = fma_f2(f, f, acc);
             }
-            pq[q] = f2_to_bf2x2(x.x, x.y);
+            // (a head that is not there: 0 rather than 0 / sqrt(eps))
+            const float ss = warp_sum(acc.x + acc.y);
+            const float rstd = h < nh ? rsqrtf(ss * (1.f / kD) + a.eps) : 0.f;
+            uint32_t pq[8];
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+              float2 x = mul_f2(mul_f2(bf2x2_to_f2(wv[q]), make_float2(rstd, rstd)), g[q]);
+              if (q >= 4) {
+                const float2 cs = rope[q - 4];
+                x = fma_f2(make_float2(x.x, x.x), cs, mul_f2(make_float2(x.y, x.y), make_float2(-cs.y, cs.x)));
+              }
+              pq[q] = f2_to_bf2x2(x.x, x.y);
+            }
+            const uint32_t sw = sw128((uint32_t)h, (uint32_t)(lane & 7));
+            st_shared16(q_base + offA + sw, pq[0], pq[1], pq[2], pq[3]);
+            st_shared16(q_base + offB + sw, pq[4], pq[5], pq[6], pq[7]);
           }
-          const uint32_t sw = sw128((uint32_t)h, (uint32_t)(lane & 7));
-          st_shared16(q_base + offA + sw, pq[0], pq[1], pq[2], pq[3]);
-          st_shared16(q_base + offB + sw, pq[4], pq[5], pq[6], pq[7]);
+          if (half == 0) load_q(1);
         }
       }
       fence_async_smem();
@@ -452,9 +458,20 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
               x = fma_f2(make_float2(x.x, x.x), make_float2(cs, -sn), mul_f2(make_float2(x.y, x.y), make_float2(sn, cs)));
             st_shared32(q_base + (uint32_t)h * kStagePitch + dd, f2_to_bf2x2(x.x, x.y));
           }
+        } else if (walk.kind == 0) {  // through the ring, which this only segment has left
+#pragma unroll
+          for (int i = 0; i < 32; ++i) st_shared32(kv_base + (uint32_t)((h0 + i) * kD + d) * 4u, __float_as_uint(v[i]));
         } else {
 #pragma unroll
           for (int i = 0; i < 32; ++i) part[2 * kH + (h0 + i) * kD + d] = v[i];
+        }
+      }
+      if (!sg.whole && walk.kind == 0) {
+        fence_async_smem();
+        named_bar(1, 256);
+        if (st < 8) {
+          bulk_s2g(part + 2 * kH + st * 8 * kD, kv_base + (uint32_t)st * 8u * kD * 4u, 8 * kD * 4);
+          bulk_commit();
         }
       }
       tc_fence_before();
@@ -557,114 +574,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
     mbar_wait(bar(kDrain), 0, abort_flag, err);
     if (lane == 0) bulk_wait0();
     __syncwarp();
-  } else if (tid < kPtr0) {
-    // =================== gather ===================
-    pdl_wait();
-    const int pt = tid - kPG0;  // 0..127
-    uint32_t gt = 0;
-    auto acquire = [&](uint32_t u) {  // chunk u's slot
-      if (u >= kSlots) mbar_wait(bar(kKVEmpty + u % kSlots), (u / kSlots - 1) & 1u, abort_flag, err);
-    };
-    while (paged_next(a, walk, sg, kKT)) {
-      for (int tile = 0; tile < sg.n_tiles; ++tile, ++gt) {
-        const uint32_t rs = gt % kAhead;
-        mbar_wait(bar(kRowFull + rs), (gt / kAhead) & 1u, abort_flag, err);
-        const unsigned long long* rp = rows + rs * kKT;
-        if (!kFp8) {
-          // a thread takes the 16-byte piece pt % 16 of eight rows' 256 bytes; a
-          // key without a row gets zeros (no branch: the copies go out together)
-          const int piece = pt & 15;
-          const uint16_t* src[kKT / 8];
-          uint32_t bytes[kKT / 8];
-#pragma unroll
-          for (int i = 0; i < kKT / 8; ++i) {
-            const unsigned long long v = rp[(pt >> 4) + 8 * i];
-            bytes[i] = v ? 16u : 0u;
-            src[i] = (v ? reinterpret_cast<const uint16_t*>(v) : a.q) + piece * 8;
-          }
-          // (rows 8 apart share their place in the swizzle)
-          const uint32_t at = (uint32_t)(piece >> 3) * kBlk + sw128(pt >> 4, piece & 7);
-          for (int c = 0; c < 4; ++c) {
-            const uint32_t u = 4 * gt + c;
-            acquire(u);
-            const uint32_t dst = kv_base + (u % kSlots) * kSlot + at;
-#pragma unroll
-            for (int i = 0; i < kKT / 8; ++i) cp_async16_or_zero(dst + 1024u * i, src[i] + c * 128, bytes[i]);
-            cp_async_arrive(bar(kKVFull + u % kSlots));
-          }
-        } else {
-          // FP8 rows: a thread takes 16 dims of four rows.  A chunk's codes are
-          // loaded while the one before is expanded (code times the block's
-          // power of two, exact in bf16) and stored; rows of the window and
-          // the RoPE dims are bf16 and copied as they are.
-          const int p8 = pt & 7;
-          unsigned long long rv[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) rv[i] = rp[(pt >> 3) + 16 * i];
-          auto load = [&](int c, uint4 (&w0)[4], uint4 (&w1)[4], uint32_t (&sc)[4]) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const uint8_t* src = reinterpret_cast<const uint8_t*>(rv[i] & ~1ull);
-              w0[i] = w1[i] = make_uint4(0, 0, 0, 0);
-              sc[i] = 0;
-              if (rv[i] & 1ull) {
-                if (c < 3 || p8 < 4) {
-                  w0[i] = *reinterpret_cast<const uint4*>(src + c * 128 + p8 * 16);
-                  sc[i] = src[kD + 64 + 4 * c + (p8 >> 1)];
-                } else {  // dims 448 + 16 (p8 - 4) ..
-                  w0[i] = *reinterpret_cast<const uint4*>(src + 448 + (p8 - 4) * 32);
-                  w1[i] = *reinterpret_cast<const uint4*>(src + 448 + (p8 - 4) * 32 + 16);
-                }
-              } else if (rv[i]) {
-                w0[i] = *reinterpret_cast<const uint4*>(src + c * 256 + p8 * 32);
-                w1[i] = *reinterpret_cast<const uint4*>(src + c * 256 + p8 * 32 + 16);
-              }
-            }
-          };
-          auto store = [&](int c, uint4 (&w0)[4], uint4 (&w1)[4], uint32_t (&sc)[4]) {
-            const uint32_t u = 4 * gt + c;
-            acquire(u);
-            const uint32_t blk = kv_base + (u % kSlots) * kSlot + (uint32_t)(p8 >> 2) * kBlk;
-            const int q0 = (2 * p8) & 7;  // 16-byte piece of the 128-byte row
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int row = (pt >> 3) + 16 * i;
-              if ((rv[i] & 1ull) && (c < 3 || p8 < 4)) {
-                const float s = mx_scale((int)sc[i]);
-                const uint32_t wd[4] = {w0[i].x, w0[i].y, w0[i].z, w0[i].w};
-                uint32_t o[8];
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                  const float2 f = mul_f2(e4m3x2_to_f2(wd[k >> 1] >> (16 * (k & 1))), make_float2(s, s));
-                  o[k] = f2_to_bf2x2(f.x, f.y);
-                }
-                w0[i] = make_uint4(o[0], o[1], o[2], o[3]);
-                w1[i] = make_uint4(o[4], o[5], o[6], o[7]);
-              }
-              st_shared16(blk + sw128(row, q0), w0[i].x, w0[i].y, w0[i].z, w0[i].w);
-              st_shared16(blk + sw128(row, q0 + 1), w1[i].x, w1[i].y, w1[i].z, w1[i].w);
-            }
-            fence_async_smem();
-            mbar_arrive(bar(kKVFull + u % kSlots));
-          };
-          uint4 wa0[4], wa1[4], wb0[4], wb1[4];
-          uint32_t sa[4], sb[4];
-          load(0, wa0, wa1, sa);
-#pragma unroll 1
-          for (int c = 0; c < 4; c += 2) {
-            load(c + 1, wb0, wb1, sb);
-            store(c, wa0, wa1, sa);
-            if (c == 0) load(2, wa0, wa1, sa);
-            store(c + 1, wb0, wb1, sb);
-          }
-        }
-        mbar_arrive(bar(kRowEmpty + rs));
-      }
-    }
-    cp_async_wait<0>();  // nothing of this block is in flight at exit
-  } else {
+  } else if (tid < kPG0) {
     // =================== row addresses ===================
-    pdl_wait();
+    // (positions and the table are inputs; the listed slots a kernel may have
+    // just written)
+    if (a.sparse) pdl_wait();
     const int key = tid - kPtr0;  // 0..63
     uint32_t gt = 0;
     while (paged_next(a, walk, sg, kKT)) {
@@ -678,6 +592,141 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
         if (gt >= kAhead) mbar_wait(bar(kRowEmpty + gt % kAhead), (gt / kAhead - 1) & 1u, abort_flag, err);
         rows[(gt % kAhead) * kKT + key] = reinterpret_cast<unsigned long long>(row) | (fp8 ? 1ull : 0ull);
         mbar_arrive(bar(kRowFull + gt % kAhead));
+      }
+    }
+  } else {
+    // =================== gather ===================
+    pdl_wait();
+    const int pt = tid - kPG0;  // 0..255
+    int left = 0;               // tiles of the segment
+    auto next_tile = [&]() {
+      if (left == 0) {
+        if (!paged_next(a, walk, sg, kKT)) return false;
+        left = sg.n_tiles;
+      }
+      --left;
+      return true;
+    };
+    auto acquire = [&](uint32_t u) {  // chunk u's slot
+      if (u >= kSlots) mbar_wait(bar(kKVEmpty + u % kSlots), (u / kSlots - 1) & 1u, abort_flag, err);
+    };
+    if (!kFp8) {
+      // a thread takes the 16-byte piece pt % 16 of four rows' 256 bytes; a
+      // key without a row gets zeros (no branch: the copies go out together)
+      constexpr int kN = kKT * 16 / kGather;
+      const int piece = pt & 15, row0 = pt >> 4;
+      // (rows 16 apart share their place in the swizzle)
+      const uint32_t at = (uint32_t)(piece >> 3) * kBlk + sw128(row0, piece & 7);
+      for (uint32_t gt = 0; next_tile(); ++gt) {
+        const uint32_t rs = gt % kAhead;
+        mbar_wait(bar(kRowFull + rs), (gt / kAhead) & 1u, abort_flag, err);
+        const uint16_t* src[kN];
+        uint32_t bytes[kN];
+#pragma unroll
+        for (int i = 0; i < kN; ++i) {
+          const unsigned long long v = rows[rs * kKT + row0 + (kGather / 16) * i];
+          bytes[i] = v ? 16u : 0u;
+          src[i] = (v ? reinterpret_cast<const uint16_t*>(v) : a.q) + piece * 8;
+        }
+        mbar_arrive(bar(kRowEmpty + rs));
+        for (int c = 0; c < 4; ++c) {
+          const uint32_t u = 4 * gt + c;
+          acquire(u);
+          const uint32_t dst = kv_base + (u % kSlots) * kSlot + at;
+#pragma unroll
+          for (int i = 0; i < kN; ++i) cp_async16_or_zero(dst + (kGather / 16) * 128u * i, src[i] + c * 128, bytes[i]);
+          cp_async_arrive(bar(kKVFull + u % kSlots));
+        }
+      }
+      cp_async_wait<0>();  // nothing of this block is in flight at exit
+    } else {
+      // FP8 rows: a thread takes 16 dims of two rows.  The codes are loaded a
+      // tile ahead, a chunk's when the tile's own have been expanded (code
+      // times the block's power of two, exact in bf16) and stored, and a row's
+      // 16 bytes of scales with them; the RoPE dims are bf16 and stored as they
+      // are.  The window's rows, two tiles of a sequence, are bf16 and loaded
+      // when they are due.
+      constexpr int kN = kKT * 8 / kGather, kStep = kGather / 8;
+      const int p8 = pt & 7, row0 = pt >> 3;
+      const bool rope = p8 >= 4;  // of the last chunk
+      uint4 w[4][kN], w3[kN], sc[kN], sc_next[kN];
+      unsigned long long rv[kN], rv_next[kN];
+      auto take_rows = [&](uint32_t gt) {
+        const uint32_t rs = gt % kAhead;
+        mbar_wait(bar(kRowFull + rs), (gt / kAhead) & 1u, abort_flag, err);
+#pragma unroll
+        for (int i = 0; i < kN; ++i) rv_next[i] = rows[rs * kKT + row0 + kStep * i];
+        mbar_arrive(bar(kRowEmpty + rs));
+#pragma unroll
+        for (int i = 0; i < kN; ++i)
+          if (rv_next[i] & 1ull) sc_next[i] = *reinterpret_cast<const uint4*>((rv_next[i] & ~1ull) + kD + 64);
+      };
+      auto load = [&](int c) {  // of the next tile
+#pragma unroll
+        for (int i = 0; i < kN; ++i)
+          if (rv_next[i] & 1ull) {
+            const uint8_t* src = reinterpret_cast<const uint8_t*>(rv_next[i] & ~1ull);
+            if (c == 3 && rope) {  // dims 448 + 16 (p8 - 4) ..
+              w[c][i] = *reinterpret_cast<const uint4*>(src + 448 + (p8 - 4) * 32);
+              w3[i] = *reinterpret_cast<const uint4*>(src + 448 + (p8 - 4) * 32 + 16);
+            } else {
+              w[c][i] = *reinterpret_cast<const uint4*>(src + c * 128 + p8 * 16);
+            }
+          }
+      };
+      bool have = next_tile();
+      if (have) {
+        take_rows(0);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) load(c);
+      }
+      const int q0 = (2 * p8) & 7;  // 16-byte piece of the 128-byte row
+      for (uint32_t gt = 0; have; ++gt) {
+#pragma unroll
+        for (int i = 0; i < kN; ++i) {
+          rv[i] = rv_next[i];
+          sc[i] = sc_next[i];
+        }
+        have = next_tile();
+        if (have) take_rows(gt + 1);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const uint32_t u = 4 * gt + c;
+          acquire(u);
+          const uint32_t blk = kv_base + (u % kSlots) * kSlot + (uint32_t)(p8 >> 2) * kBlk;
+#pragma unroll
+          for (int i = 0; i < kN; ++i) {
+            const int row = row0 + kStep * i;
+            uint4 x = make_uint4(0, 0, 0, 0), y = make_uint4(0, 0, 0, 0);
+            if (!(rv[i] & 1ull)) {
+              if (rv[i]) {
+                const uint4* src = reinterpret_cast<const uint4*>(rv[i] + c * 256 + p8 * 32);
+                x = src[0];
+                y = src[1];
+              }
+            } else if (c == 3 && rope) {
+              x = w[c][i];
+              y = w3[i];
+            } else {
+              const uint32_t s4 = c == 0 ? sc[i].x : c == 1 ? sc[i].y : c == 2 ? sc[i].z : sc[i].w;
+              const float s = mx_scale((int)(s4 >> (8 * (p8 >> 1)) & 255u));
+              const uint32_t wd[4] = {w[c][i].x, w[c][i].y, w[c][i].z, w[c][i].w};
+              uint32_t o[8];
+#pragma unroll
+              for (int k = 0; k < 8; ++k) {
+                const float2 f = mul_f2(e4m3x2_to_f2(wd[k >> 1] >> (16 * (k & 1))), make_float2(s, s));
+                o[k] = f2_to_bf2x2(f.x, f.y);
+              }
+              x = make_uint4(o[0], o[1], o[2], o[3]);
+              y = make_uint4(o[4], o[5], o[6], o[7]);
+            }
+            st_shared16(blk + sw128(row, q0), x.x, x.y, x.z, x.w);
+            st_shared16(blk + sw128(row, q0 + 1), y.x, y.y, y.z, y.w);
+          }
+          fence_async_smem();
+          mbar_arrive(bar(kKVFull + u % kSlots));
+          if (have) load(c);
+        }
       }
     }
   }
