@@ -11,14 +11,16 @@
 // sequences: every block of the attention finds its own place.
 //   Up to as many items as blocks: the shortest T for which the blocks do when
 //   an item of n tiles is cut into ceil(n / T) equal pieces, a block each, and
-//   items of up to T / 2 tiles share blocks, whole, each counted three tiles
+//   items of up to T / 2 tiles share blocks, whole, each counted six tiles
 //   longer: that is about what a segment costs besides its tiles (its q^, the
 //   filling of the pipeline, the output), and why pieces a little longer than
 //   the average beat equal shares.  A piece costs, on top, a float accumulator
 //   written (128 KiB for 64 heads x 512) and read by the joining kernel.
-//   More items, or lengths with which T would exceed the average by more than
-//   a segment's cost: their tiles stand in one row, cut into equal ranges, but
-//   a cut that would fall into a short item moves to its nearer end.
+//   More items: whole items share the blocks in the same way, if the longest
+//   block that this makes is no longer than with the third way:
+//   The tiles of all items stand in one row, cut into equal ranges (a cut that
+//   would fall into a short item moves to its nearer end).  This is also for
+//   lengths with which T would exceed the average by more than a segment costs.
 // A block's piece of an item is a segment; an item that one block holds whole
 // is finished there, the others are joined from their segments.
 #pragma once
@@ -122,7 +124,8 @@ __device__ __forceinline__ int paged_item_seq(const PagedArgs& a, int item) {
 
 // Items of at most this many tiles are not cut, and no piece is shorter.
 constexpr int kPagedWhole = 4, kPagedLeast = 2;
-constexpr int kPagedCost = 3;  // of a segment, in tiles
+constexpr int kPagedCost = 6;  // of a segment besides its tiles, in tiles (measured: 14 us a second segment)
+constexpr int kPagedJoin = 4;  // of the joining, in tiles
 constexpr int kPagedChunks = 8;  // of 32 sequences, that a warp holds in registers (296 blocks at most)
 
 // More items than blocks: the blocks that take part, where block c's range
@@ -209,8 +212,9 @@ __device__ __forceinline__ PagedRange paged_range(const PagedArgs& a, int c, int
     // (T = the longest item's tiles fits: one block an item or fewer)
     int yes = max(kPagedLeast, (total + a.G - 1) / a.G);
     if (!fits(yes)) {
-      int no = yes;
-      yes = max(most, no + 1);
+      int no = yes;  // (sum n / T + 1 over the items bounds the pieces)
+      yes = max(no + 1, a.G > items ? min(most, (total + a.G - items - 1) / (a.G - items)) : most);
+      if (!fits(yes)) yes = max(most, yes);  // (an item a block, or fewer blocks)
 #pragma unroll 1
       while (yes - no > 1) {
         const int mid = (yes + no) >> 1;
@@ -265,12 +269,51 @@ __device__ __forceinline__ PagedRange paged_range(const PagedArgs& a, int c, int
     }
     if (!rows) return r;
   }
-  r.kind = 2;
   int v = 0, inc = 0;
   if (items > a.G) {
+    int most = 0, some = 0;  // longest item, items with tiles
 #pragma unroll 1
-    for (int b0 = 0; b0 < a.B; b0 += 32) total += sum(tiles_at(b0)) * hg;
+    for (int b0 = 0; b0 < a.B; b0 += 32) {
+      v = tiles_at(b0);
+      total += v;
+      most = max(most, v);
+      some += v > 0;
+    }
+    total = sum(total) * hg;
+    some = sum(some) * hg;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
+    const int64_t costs = (int64_t)total + (int64_t)some * kPagedCost;
+    const int share = (int)((costs + a.G - 1) / a.G), longest = most + kPagedCost;
+    // with items that are long next to a share, as many of the longest as one takes
+    const int64_t shared = 4 * longest > share ? (int64_t)((share + longest - 1) / longest) * longest : (int64_t)share + longest / 2;
+    if (shared <= total / a.G + 2 * kPagedCost + kPagedJoin) {
+      const int64_t s0 = (int64_t)c * 2 * share;
+      if (s0 > 2 * costs) return r;
+      r.T = 2 * most;
+      r.stop = (int)(s0 + 2 * share);
+      int before = 0;
+#pragma unroll 1
+      for (int b0 = 0; b0 < a.B; b0 += 32) {
+        v = tiles_at(b0);
+        const int w = v > 0 ? v + kPagedCost : 0, wi = scan(w * hg);
+        // the sequence's last group lies behind the share's begin
+        const unsigned int here = __ballot_sync(0xffffffffu, w > 0 && 2 * (before + wi) - w >= (int)s0);
+        if (here) {
+          const int l = __ffs(here) - 1;
+          int g = 0, d = before + __shfl_sync(0xffffffffu, wi - w * hg, l);
+          const int w_l = __shfl_sync(0xffffffffu, w, l);
+          for (; 2 * d + w_l < (int)s0; d += w_l) ++g;
+          r.item = (b0 + l) * hg + g;
+          r.done = d;
+          return r;
+        }
+        before += __shfl_sync(0xffffffffu, wi, 31);
+      }
+      return r;
+    }
   }
+  r.kind = 2;
   r.total = total;
   r.ge = max(1, paged_blocks(total, a.G));
   r.raw0 = paged_start(c, total, r.ge);

@@ -34,11 +34,12 @@ using namespace tc;
 
 constexpr int kH = 64, kD = 512;
 constexpr int kKT = 64;               // keys per tile
-constexpr int kThreads = 608;
+constexpr int kThreads = 640;
 constexpr int kMmaWarp = 8;
 constexpr int kPtr0 = 288;            // first address thread (warps 9-10)
 constexpr int kPG0 = 352;             // first gathering thread (warps 11-18)
-constexpr int kGather = kThreads - kPG0;
+constexpr int kGather = 256;
+constexpr int kFenceWarp = 19;
 constexpr int kSlots = 9;             // ring of 128-dim chunks
 constexpr int kAhead = 4;             // tiles of row addresses
 constexpr float kLog2e = 1.4426950408889634f;
@@ -51,7 +52,7 @@ constexpr uint32_t kOffKV = 0;
 constexpr uint32_t kOffQ = kSlots * kSlot;       // 8 blocks x [64 heads][128 B]
 constexpr uint32_t kOffP = kOffQ + 65536;        // [64 keys][128 B]
 constexpr uint32_t kOffBar = kOffP + kBlk;
-constexpr uint32_t kOffMisc = kOffBar + 320;     // abort flag, TMEM address, the block's range
+constexpr uint32_t kOffMisc = kOffBar + 384;     // abort flag, TMEM address, the block's range
 constexpr uint32_t kOffRow = kOffMisc + 128;      // [4 tiles][64] row addresses, bit 0: FP8
 constexpr uint32_t kOffRed = kOffRow + kAhead * kKT * 8;  // [4][64] floats
 constexpr uint32_t kOffMrun = kOffRed + 1024;
@@ -68,24 +69,44 @@ constexpr uint32_t kStagePitch = 1088;
 static_assert(kH * kStagePitch <= 65536 + kBlk && kH * kD * 4 <= kSlots * kSlot, "output stages");
 
 enum Bar {
-  kKVFull = 0, kKVEmpty = kKVFull + kSlots, kRowFull = kKVEmpty + kSlots, kRowEmpty = kRowFull + kAhead,
+  kKVLanded = 0, kKVFull = kKVLanded + kSlots, kKVEmpty = kKVFull + kSlots, kRowFull = kKVEmpty + kSlots, kRowEmpty = kRowFull + kAhead,
   kQFull = kRowEmpty + kAhead, kSFull0, kSFull1, kPFull, kPVDone, kEpiDone, kDrain, kNumBars
 };
-static_assert(kNumBars * 8 <= 320, "barriers");
+static_assert(kNumBars * 8 <= 384, "barriers");
 
 constexpr uint32_t kIdescQK = idesc_bf16(64, 64, 0, 0);
 constexpr uint32_t kIdescPV = idesc_bf16(128, 64, 1, 1);
 
-// An MMA / a commit by one elected lane of a converged warp.  The election
-// gives the same lane each time, so that the commits cover the MMAs.
-__device__ __forceinline__ void mma_bf16_elect(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                               uint32_t accumulate) {
+// MMAs and commits by one elected lane of a converged warp.  The election gives
+// the same lane each time, so that the commits cover the MMAs.  A chunk's MMAs
+// are one statement, with the low words of the descriptors (the high words are
+// the same): da and db in 16-byte units, and what each MMA adds to them.
+#define DS4A_MMA(off, pred)                                                            \
+  " add.u32 x, %1, " #off ";\n add.u32 y, %2, " #off ";\n"                             \
+  " mov.b64 da, {x, %3};\n mov.b64 db, {y, %3};\n"                                     \
+  " @q tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %4, " pred ";\n"
+// S^T += 128 dims: eight MMAs, 32 bytes of a 128-byte row each, then the next 64 dims' block
+__device__ __forceinline__ void mma_qk_chunk(uint32_t d_tmem, uint32_t da, uint32_t db, uint32_t hi, uint32_t idesc,
+                                             uint32_t accumulate) {
   asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n elect.sync _|q, 0xffffffff;\n"
-      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      "{\n .reg .pred p, t, q;\n .reg .b64 da, db;\n .reg .b32 x, y;\n"
+      " setp.ne.b32 p, %5, 0;\n setp.eq.b32 t, 0, 0;\n elect.sync _|q, 0xffffffff;\n"
+      DS4A_MMA(0, "p") DS4A_MMA(2, "t") DS4A_MMA(4, "t") DS4A_MMA(6, "t")
+      DS4A_MMA(512, "t") DS4A_MMA(514, "t") DS4A_MMA(516, "t") DS4A_MMA(518, "t")
+      "}\n" ::"r"(d_tmem), "r"(da), "r"(db), "r"(hi), "r"(idesc), "r"(accumulate)
       : "memory");
 }
+// O^T of 128 dims += 64 keys: four MMAs, 16 keys each
+__device__ __forceinline__ void mma_pv_chunk(uint32_t d_tmem, uint32_t da, uint32_t db, uint32_t hi, uint32_t idesc,
+                                             uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p, t, q;\n .reg .b64 da, db;\n .reg .b32 x, y;\n"
+      " setp.ne.b32 p, %5, 0;\n setp.eq.b32 t, 0, 0;\n elect.sync _|q, 0xffffffff;\n"
+      DS4A_MMA(0, "p") DS4A_MMA(128, "t") DS4A_MMA(256, "t") DS4A_MMA(384, "t")
+      "}\n" ::"r"(d_tmem), "r"(da), "r"(db), "r"(hi), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+#undef DS4A_MMA
 __device__ __forceinline__ void mma_commit_elect(uint32_t bar) {
   asm volatile(
       "{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n"
@@ -124,9 +145,7 @@ __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
   return ok != 0;
 }
 
-// Arrive on the mbarrier when this thread's cp.async so far have landed.  (The
-// rows are written in the generic proxy: the MMA's thread fences the proxies
-// after it has waited for the barrier.)
+// Arrive on the mbarrier when this thread's cp.async so far have landed.
 __device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
@@ -154,14 +173,16 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
   float* sink_s = reinterpret_cast<float*>(smem + kOffSink);
   float2* rope_s = reinterpret_cast<float2*>(smem + kOffRope);
 
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // (the same in the warp, as the compiler sees it)
   unsigned int* err = a.err;
 
   pdl_trigger();
   if (tid == 0) {
     *abort_flag = 0;
     for (int i = 0; i < kSlots; ++i) {
-      mbar_init(bar(kKVFull + i), kGather);
+      mbar_init(bar(kKVLanded + i), kFp8 ? kGather / 2 : kGather);
+      mbar_init(bar(kKVFull + i), 1);
       mbar_init(bar(kKVEmpty + i), 1);
     }
     for (int i = 0; i < kAhead; ++i) {
@@ -493,52 +514,50 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
   } else if (warp == kMmaWarp) {
     // =================== MMA issuer ===================
     pdl_wait();
-    const uint64_t qk_a0 = sdesc_sw128(kv_base, 16, 1024);
-    const uint64_t qk_b0 = sdesc_sw128(q_base, 16, 1024);
-    const uint64_t pv_a0 = sdesc_sw128(kv_base, kBlk, 1024);
-    const uint64_t pv_b0 = sdesc_sw128(p_base, kBlk, 1024);
+    // low words of the descriptors; the strides between 8-row groups, the
+    // swizzle and the rest of the high words are the same
+    const uint32_t qk_a = (uint32_t)sdesc_sw128(kv_base, 16, 1024), qk_b = (uint32_t)sdesc_sw128(q_base, 16, 1024);
+    const uint32_t pv_a = (uint32_t)sdesc_sw128(kv_base, kBlk, 1024), pv_b = (uint32_t)sdesc_sw128(p_base, kBlk, 1024);
+    const uint32_t sd_hi = (uint32_t)(sdesc_sw128(kv_base, 16, 1024) >> 32);
     // The whole warp runs this loop and an elected lane issues: with operands
     // that are the same in all lanes an MMA of this shape goes out every 48
     // cycles, what its 6 KiB of shared memory take; from a branch of one lane
     // it was 54 to 90.
     uint32_t gt = 0, active = 0;
-    while (paged_next(a, walk, sg, kKT)) {
+    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+    while (__any_sync(0xffffffffu, paged_next(a, walk, sg, kKT))) {
+      const int n_tiles = __shfl_sync(0xffffffffu, sg.n_tiles, 0);
       auto qk_chunk = [&](uint32_t g, int c) {
         const uint32_t slot = (4 * g + c) % kSlots;
-        const uint32_t d_s = tmem + (g & 1u) * 64u;
-        const uint64_t da = qk_a0 + ((slot * kSlot) >> 4), db = qk_b0 + ((2u * c * 8192u) >> 4);
-#pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
-          mma_bf16_elect(d_s, da + (((kk >> 2) * kBlk + (kk & 3) * 32u) >> 4), db + (((kk >> 2) * 8192u + (kk & 3) * 32u) >> 4),
-                         kIdescQK, kk != 0 || c != 0 ? 1u : 0u);
+        mma_qk_chunk(tm + (g & 1u) * 64u, qk_a + ((slot * kSlot) >> 4), qk_b + ((2u * c * 8192u) >> 4), sd_hi, kIdescQK, c);
       };
       auto kv_full = [&](uint32_t g, int c) { return bar(kKVFull + (4 * g + c) % kSlots); };
       auto kv_phase = [&](uint32_t g, int c) { return ((4 * g + c) / kSlots) & 1u; };
       mbar_wait(bar(kQFull), active & 1u, abort_flag, err);
       tc_fence_after();
       int qc = 0;  // chunks of the tile's first product that are issued
-      for (int tile = 0; tile < sg.n_tiles; ++tile, ++gt) {
+      for (int tile = 0; tile < n_tiles; ++tile, ++gt) {
         if (qc < 4) {
           for (; qc < 4; ++qc) {
             mbar_wait(kv_full(gt, qc), kv_phase(gt, qc), abort_flag, err);
             __syncwarp();
             tc_fence_after();
-            fence_async_smem();
             qk_chunk(gt, qc);
           }
           mma_commit_elect(bar(kSFull0 + (gt & 1u)));
         }
         // until P^T comes: the next tile's first product, as it arrives
         qc = 0;
-        const bool more = tile + 1 < sg.n_tiles;
+        const bool more = tile + 1 < n_tiles;
         while (more && qc < 4) {
           const bool p_here = mbar_test(bar(kPFull), gt & 1u) || *abort_flag;
-          if (__any_sync(0xffffffffu, p_here)) break;
-          if (__all_sync(0xffffffffu, mbar_test(kv_full(gt + 1, qc), kv_phase(gt + 1, qc)))) {
+          const bool kv_here = mbar_test(kv_full(gt + 1, qc), kv_phase(gt + 1, qc));
+          if (__all_sync(0xffffffffu, kv_here)) {
             tc_fence_after();
-            fence_async_smem();
             qk_chunk(gt + 1, qc);
             if (++qc == 4) mma_commit_elect(bar(kSFull0 + ((gt + 1) & 1u)));
+          } else if (__any_sync(0xffffffffu, p_here)) {
+            break;
           }
         }
         mbar_wait(bar(kPFull), gt & 1u, abort_flag, err);
@@ -554,11 +573,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           const uint32_t slot = (4 * gt + c) % kSlots;
-          const uint64_t da = pv_a0 + ((slot * kSlot) >> 4);
-#pragma unroll
-          for (int kk = 0; kk < kKT / 16; ++kk)
-            mma_bf16_elect(tmem + 128u + 64u * c, da + ((kk * 2048u) >> 4), pv_b0 + ((kk * 2048u) >> 4), kIdescPV,
-                           kk == 0 ? acc0 : 1u);
+          mma_pv_chunk(tm + 128u + 64u * c, pv_a + ((slot * kSlot) >> 4), pv_b, sd_hi, kIdescPV, acc0);
           mma_commit_elect(bar(kKVEmpty + slot));
         }
         if (a.weights) {
@@ -594,7 +609,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
         mbar_arrive(bar(kRowFull + gt % kAhead));
       }
     }
-  } else {
+  } else if (warp != kFenceWarp) {
     // =================== gather ===================
     pdl_wait();
     const int pt = tid - kPG0;  // 0..255
@@ -635,98 +650,81 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
           const uint32_t dst = kv_base + (u % kSlots) * kSlot + at;
 #pragma unroll
           for (int i = 0; i < kN; ++i) cp_async16_or_zero(dst + (kGather / 16) * 128u * i, src[i] + c * 128, bytes[i]);
-          cp_async_arrive(bar(kKVFull + u % kSlots));
+          cp_async_arrive(bar(kKVLanded + u % kSlots));
         }
       }
       cp_async_wait<0>();  // nothing of this block is in flight at exit
     } else {
-      // FP8 rows: a thread takes 16 dims of two rows.  The codes are loaded a
-      // tile ahead, a chunk's when the tile's own have been expanded (code
-      // times the block's power of two, exact in bf16) and stored, and a row's
-      // 16 bytes of scales with them; the RoPE dims are bf16 and stored as they
-      // are.  The window's rows, two tiles of a sequence, are bf16 and loaded
-      // when they are due.
-      constexpr int kN = kKT * 8 / kGather, kStep = kGather / 8;
-      const int p8 = pt & 7, row0 = pt >> 3;
-      const bool rope = p8 >= 4;  // of the last chunk
-      uint4 w[4][kN], w3[kN], sc[kN], sc_next[kN];
-      unsigned long long rv[kN], rv_next[kN];
-      auto take_rows = [&](uint32_t gt) {
+      // FP8 rows: two warps a chunk, a thread 16 dims of eight rows.  The codes
+      // are loaded a tile ahead, when the tile's own have been expanded (code
+      // times the block's power of two, exact in bf16) and stored; the RoPE
+      // dims and the window's rows are bf16 and copied as they are.
+      constexpr int kN = 8;
+      const int c = pt >> 6, p8 = pt & 7, row0 = (pt >> 3) & 7;  // rows row0 + 8 i (which share their place in the swizzle)
+      const bool rope = c == 3 && p8 >= 4;  // dims 448 + 16 (p8 - 4) ..
+      uint4 w[kN];
+      uint32_t sc[kN];
+      auto load = [&](uint32_t gt) {
         const uint32_t rs = gt % kAhead;
         mbar_wait(bar(kRowFull + rs), (gt / kAhead) & 1u, abort_flag, err);
-#pragma unroll
-        for (int i = 0; i < kN; ++i) rv_next[i] = rows[rs * kKT + row0 + kStep * i];
-        mbar_arrive(bar(kRowEmpty + rs));
-#pragma unroll
-        for (int i = 0; i < kN; ++i)
-          if (rv_next[i] & 1ull) sc_next[i] = *reinterpret_cast<const uint4*>((rv_next[i] & ~1ull) + kD + 64);
-      };
-      auto load = [&](int c) {  // of the next tile
-#pragma unroll
-        for (int i = 0; i < kN; ++i)
-          if (rv_next[i] & 1ull) {
-            const uint8_t* src = reinterpret_cast<const uint8_t*>(rv_next[i] & ~1ull);
-            if (c == 3 && rope) {  // dims 448 + 16 (p8 - 4) ..
-              w[c][i] = *reinterpret_cast<const uint4*>(src + 448 + (p8 - 4) * 32);
-              w3[i] = *reinterpret_cast<const uint4*>(src + 448 + (p8 - 4) * 32 + 16);
-            } else {
-              w[c][i] = *reinterpret_cast<const uint4*>(src + c * 128 + p8 * 16);
-            }
-          }
-      };
-      bool have = next_tile();
-      if (have) {
-        take_rows(0);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) load(c);
-      }
-      const int q0 = (2 * p8) & 7;  // 16-byte piece of the 128-byte row
-      for (uint32_t gt = 0; have; ++gt) {
+        if (rope) return;
 #pragma unroll
         for (int i = 0; i < kN; ++i) {
-          rv[i] = rv_next[i];
-          sc[i] = sc_next[i];
-        }
-        have = next_tile();
-        if (have) take_rows(gt + 1);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const uint32_t u = 4 * gt + c;
-          acquire(u);
-          const uint32_t blk = kv_base + (u % kSlots) * kSlot + (uint32_t)(p8 >> 2) * kBlk;
-#pragma unroll
-          for (int i = 0; i < kN; ++i) {
-            const int row = row0 + kStep * i;
-            uint4 x = make_uint4(0, 0, 0, 0), y = make_uint4(0, 0, 0, 0);
-            if (!(rv[i] & 1ull)) {
-              if (rv[i]) {
-                const uint4* src = reinterpret_cast<const uint4*>(rv[i] + c * 256 + p8 * 32);
-                x = src[0];
-                y = src[1];
-              }
-            } else if (c == 3 && rope) {
-              x = w[c][i];
-              y = w3[i];
-            } else {
-              const uint32_t s4 = c == 0 ? sc[i].x : c == 1 ? sc[i].y : c == 2 ? sc[i].z : sc[i].w;
-              const float s = mx_scale((int)(s4 >> (8 * (p8 >> 1)) & 255u));
-              const uint32_t wd[4] = {w[c][i].x, w[c][i].y, w[c][i].z, w[c][i].w};
-              uint32_t o[8];
-#pragma unroll
-              for (int k = 0; k < 8; ++k) {
-                const float2 f = mul_f2(e4m3x2_to_f2(wd[k >> 1] >> (16 * (k & 1))), make_float2(s, s));
-                o[k] = f2_to_bf2x2(f.x, f.y);
-              }
-              x = make_uint4(o[0], o[1], o[2], o[3]);
-              y = make_uint4(o[4], o[5], o[6], o[7]);
-            }
-            st_shared16(blk + sw128(row, q0), x.x, x.y, x.z, x.w);
-            st_shared16(blk + sw128(row, q0 + 1), y.x, y.y, y.z, y.w);
+          const unsigned long long v = rows[rs * kKT + row0 + 8 * i];
+          if (v & 1ull) {
+            const uint8_t* src = reinterpret_cast<const uint8_t*>(v & ~1ull);
+            w[i] = *reinterpret_cast<const uint4*>(src + c * 128 + p8 * 16);
+            sc[i] = src[kD + 64 + 4 * c + (p8 >> 1)];
           }
-          fence_async_smem();
-          mbar_arrive(bar(kKVFull + u % kSlots));
-          if (have) load(c);
         }
+      };
+      const uint32_t blk = (uint32_t)(p8 >> 2) * kBlk;
+      const uint32_t at0 = blk + sw128(row0, (2 * p8) & 7), at1 = blk + sw128(row0, ((2 * p8) & 7) + 1);
+      bool have = next_tile();
+      if (have) load(0);
+      for (uint32_t gt = 0; have; ++gt) {
+        const uint32_t u = 4 * gt + c, slot = kv_base + (u % kSlots) * kSlot;
+        acquire(u);
+#pragma unroll
+        for (int i = 0; i < kN; ++i) {
+          const unsigned long long v = rows[(gt % kAhead) * kKT + row0 + 8 * i];
+          const uint32_t d0 = slot + at0 + 1024u * i, d1 = slot + at1 + 1024u * i;
+          if ((v & 1ull) && !rope) {
+            const float s = mx_scale((int)sc[i]);
+            const uint32_t wd[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+            uint32_t o[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const float2 f = mul_f2(e4m3x2_to_f2(wd[k >> 1] >> (16 * (k & 1))), make_float2(s, s));
+              o[k] = f2_to_bf2x2(f.x, f.y);
+            }
+            st_shared16(d0, o[0], o[1], o[2], o[3]);
+            st_shared16(d1, o[4], o[5], o[6], o[7]);
+          } else {
+            const uint8_t* src = reinterpret_cast<const uint8_t*>(v & ~1ull) +
+                                 ((v & 1ull) ? 448 + (p8 - 4) * 32 : c * 256 + p8 * 32);
+            cp_async16_or_zero(d0, v ? src : reinterpret_cast<const uint8_t*>(a.q), v ? 16u : 0u);
+            cp_async16_or_zero(d1, v ? src + 16 : reinterpret_cast<const uint8_t*>(a.q), v ? 16u : 0u);
+          }
+        }
+        mbar_arrive(bar(kRowEmpty + gt % kAhead));
+        mbar_arrive(bar(kKVLanded + u % kSlots));
+        cp_async_arrive(bar(kKVLanded + u % kSlots));
+        have = next_tile();
+        if (have) load(gt + 1);
+      }
+      cp_async_wait<0>();
+    }
+  } else {
+    // =================== landed rows to the MMAs ===================
+    // The rows are written in the generic proxy.  The fence between the proxies
+    // costs 0.2 us a chunk in the issuing warp; here it is off its path.
+    uint32_t u = 0;
+    while (paged_next(a, walk, sg, kKT)) {
+      for (int i = 4 * sg.n_tiles; i > 0; --i, ++u) {
+        mbar_wait(bar(kKVLanded + u % kSlots), (u / kSlots) & 1u, abort_flag, err);
+        fence_async_smem();
+        if (lane == 0) mbar_arrive(bar(kKVFull + u % kSlots));
       }
     }
   }
