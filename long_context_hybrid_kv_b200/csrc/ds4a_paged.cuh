@@ -356,6 +356,7 @@ struct PagedSegment {
   int item, b, g;
   int tile0, n_tiles;  // first tile in the item; how many
   bool whole;
+  bool alone;    // the block's only segment, a piece
   int slot;      // of a partial result: 1 if the item begins behind the start of the block's range, else 0
   int cut_last;  // the item's last block if it begins here and goes on, else -1
   PagedSeq seq;
@@ -371,6 +372,7 @@ __device__ __forceinline__ bool paged_next(const PagedArgs& a, PagedRange& w, Pa
     const int n = paged_tiles(s.seq, kt);
     s.slot = 0;
     s.cut_last = -1;
+    s.alone = w.kind == 0;
     if (w.kind == 0) {
       s.tile0 = w.t0;
       s.n_tiles = w.t1 - w.t0;

@@ -42,6 +42,7 @@ constexpr int kGather = 256;
 constexpr int kFenceWarp = 19;
 constexpr int kSlots = 9;             // ring of 128-dim chunks
 constexpr int kAhead = 4;             // tiles of row addresses
+constexpr int kSegs = 8;              // segments made known: the address warps are at most five tiles, so segments, ahead of the rest
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kRescaleLog2 = 8.0f;  // O^T is rescaled when a head's maximum grows by more than 2^8
 constexpr float kNoRef = -1e30f;      // reference of a head that has seen no key: finite, below any logit
@@ -52,7 +53,8 @@ constexpr uint32_t kOffKV = 0;
 constexpr uint32_t kOffQ = kSlots * kSlot;       // 8 blocks x [64 heads][128 B]
 constexpr uint32_t kOffP = kOffQ + 65536;        // [64 keys][128 B]
 constexpr uint32_t kOffBar = kOffP + kBlk;
-constexpr uint32_t kOffMisc = kOffBar + 384;     // abort flag, TMEM address, the block's range
+constexpr uint32_t kOffSeg = kOffBar + 448;         // segments
+constexpr uint32_t kOffMisc = kOffSeg + kSegs * 64;     // abort flag, TMEM address, the block's range
 constexpr uint32_t kOffRow = kOffMisc + 128;      // [4 tiles][64] row addresses, bit 0: FP8
 constexpr uint32_t kOffRed = kOffRow + kAhead * kKT * 8;  // [4][64] floats
 constexpr uint32_t kOffMrun = kOffRed + 1024;
@@ -60,7 +62,8 @@ constexpr uint32_t kOffAlpha = kOffMrun + 256;
 constexpr uint32_t kOffInv = kOffAlpha + 256;
 constexpr uint32_t kOffSink = kOffInv + 256;
 constexpr uint32_t kOffRope = kOffSink + 256;    // [128] (cos, sin) of the segment's position
-constexpr uint32_t kSmemBytes = kOffRope + 1024 + 1024;
+constexpr uint32_t kOffG = kOffRope + 1024;  // [512] norm weights
+constexpr uint32_t kSmemBytes = kOffG + 2048 + 1024;
 static_assert(kSmemBytes <= 232448, "shared memory of a block");
 // The finished output goes out through the q^ and P^T buffers, a head's 1024
 // bytes 1088 apart (the two heads that a warp writes at a time then lie in
@@ -70,9 +73,9 @@ static_assert(kH * kStagePitch <= 65536 + kBlk && kH * kD * 4 <= kSlots * kSlot,
 
 enum Bar {
   kKVLanded = 0, kKVFull = kKVLanded + kSlots, kKVEmpty = kKVFull + kSlots, kRowFull = kKVEmpty + kSlots, kRowEmpty = kRowFull + kAhead,
-  kQFull = kRowEmpty + kAhead, kSFull0, kSFull1, kPFull, kPVDone, kEpiDone, kDrain, kNumBars
+  kSegFull = kRowEmpty + kAhead, kQFull = kSegFull + kSegs, kSFull0, kSFull1, kPFull, kPVDone, kEpiDone, kDrain, kNumBars
 };
-static_assert(kNumBars * 8 <= 384, "barriers");
+static_assert(kNumBars * 8 <= 448 && sizeof(PagedSegment) <= 64, "barriers");
 
 constexpr uint32_t kIdescQK = idesc_bf16(64, 64, 0, 0);
 constexpr uint32_t kIdescPV = idesc_bf16(128, 64, 1, 1);
@@ -81,36 +84,38 @@ constexpr uint32_t kIdescPV = idesc_bf16(128, 64, 1, 1);
 // the same lane each time, so that the commits cover the MMAs.  A chunk's MMAs
 // are one statement, with the low words of the descriptors (the high words are
 // the same): da and db in 16-byte units, and what each MMA adds to them.
+// (go = 0 issues nothing)
 #define DS4A_MMA(off, pred)                                                            \
   " add.u32 x, %1, " #off ";\n add.u32 y, %2, " #off ";\n"                             \
   " mov.b64 da, {x, %3};\n mov.b64 db, {y, %3};\n"                                     \
   " @q tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %4, " pred ";\n"
 // S^T += 128 dims: eight MMAs, 32 bytes of a 128-byte row each, then the next 64 dims' block
 __device__ __forceinline__ void mma_qk_chunk(uint32_t d_tmem, uint32_t da, uint32_t db, uint32_t hi, uint32_t idesc,
-                                             uint32_t accumulate) {
+                                             uint32_t accumulate, uint32_t go) {
   asm volatile(
-      "{\n .reg .pred p, t, q;\n .reg .b64 da, db;\n .reg .b32 x, y;\n"
-      " setp.ne.b32 p, %5, 0;\n setp.eq.b32 t, 0, 0;\n elect.sync _|q, 0xffffffff;\n"
+      "{\n .reg .pred p, t, q, g;\n .reg .b64 da, db;\n .reg .b32 x, y;\n"
+      " setp.ne.b32 p, %5, 0;\n setp.eq.b32 t, 0, 0;\n elect.sync _|q, 0xffffffff;\n setp.ne.b32 g, %6, 0;\n and.pred q, q, g;\n"
       DS4A_MMA(0, "p") DS4A_MMA(2, "t") DS4A_MMA(4, "t") DS4A_MMA(6, "t")
       DS4A_MMA(512, "t") DS4A_MMA(514, "t") DS4A_MMA(516, "t") DS4A_MMA(518, "t")
-      "}\n" ::"r"(d_tmem), "r"(da), "r"(db), "r"(hi), "r"(idesc), "r"(accumulate)
+      "}\n" ::"r"(d_tmem), "r"(da), "r"(db), "r"(hi), "r"(idesc), "r"(accumulate), "r"(go)
       : "memory");
 }
 // O^T of 128 dims += 64 keys: four MMAs, 16 keys each
 __device__ __forceinline__ void mma_pv_chunk(uint32_t d_tmem, uint32_t da, uint32_t db, uint32_t hi, uint32_t idesc,
-                                             uint32_t accumulate) {
+                                             uint32_t accumulate, uint32_t go) {
   asm volatile(
-      "{\n .reg .pred p, t, q;\n .reg .b64 da, db;\n .reg .b32 x, y;\n"
-      " setp.ne.b32 p, %5, 0;\n setp.eq.b32 t, 0, 0;\n elect.sync _|q, 0xffffffff;\n"
+      "{\n .reg .pred p, t, q, g;\n .reg .b64 da, db;\n .reg .b32 x, y;\n"
+      " setp.ne.b32 p, %5, 0;\n setp.eq.b32 t, 0, 0;\n elect.sync _|q, 0xffffffff;\n setp.ne.b32 g, %6, 0;\n and.pred q, q, g;\n"
       DS4A_MMA(0, "p") DS4A_MMA(128, "t") DS4A_MMA(256, "t") DS4A_MMA(384, "t")
-      "}\n" ::"r"(d_tmem), "r"(da), "r"(db), "r"(hi), "r"(idesc), "r"(accumulate)
+      "}\n" ::"r"(d_tmem), "r"(da), "r"(db), "r"(hi), "r"(idesc), "r"(accumulate), "r"(go)
       : "memory");
 }
 #undef DS4A_MMA
-__device__ __forceinline__ void mma_commit_elect(uint32_t bar) {
+__device__ __forceinline__ void mma_commit_elect(uint32_t bar, uint32_t go = 1u) {
   asm volatile(
-      "{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n"
-      " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(bar)
+      "{\n .reg .pred q, g;\n elect.sync _|q, 0xffffffff;\n setp.ne.b32 g, %1, 0;\n and.pred q, q, g;\n"
+      " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(bar),
+      "r"(go)
       : "memory");
 }
 
@@ -145,6 +150,14 @@ __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
   return ok != 0;
 }
 
+// the low half at dst, the high half kPitch behind it
+template <uint32_t kPitch>
+__device__ __forceinline__ void st_shared_halves(uint32_t dst, uint32_t v) {
+  asm volatile("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %1;\n st.shared.b16 [%0], l;\n st.shared.b16 [%0 + %2], h;\n}\n" ::"r"(dst),
+               "r"(v), "n"(kPitch)
+               : "memory");
+}
+
 // Arrive on the mbarrier when this thread's cp.async so far have landed.
 __device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
@@ -164,13 +177,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
   auto bar = [&](int i) { return sbase + kOffBar + 8u * (uint32_t)i; };
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kOffMisc);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kOffMisc + 8);
-  PagedRange* s_range = reinterpret_cast<PagedRange*>(smem + kOffMisc + 16);
   unsigned long long* rows = reinterpret_cast<unsigned long long*>(smem + kOffRow);
   float* red = reinterpret_cast<float*>(smem + kOffRed);
   float* mrun = reinterpret_cast<float*>(smem + kOffMrun);
   float* alpha_s = reinterpret_cast<float*>(smem + kOffAlpha);
   float* inv_s = reinterpret_cast<float*>(smem + kOffInv);
   float* sink_s = reinterpret_cast<float*>(smem + kOffSink);
+  float* g_s = reinterpret_cast<float*>(smem + kOffG);
   float2* rope_s = reinterpret_cast<float2*>(smem + kOffRope);
 
   const int tid = threadIdx.x, lane = tid & 31;
@@ -189,6 +202,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
       mbar_init(bar(kRowFull + i), kKT);
       mbar_init(bar(kRowEmpty + i), kGather + 64);  // the gatherers, and 64 softmax threads for all
     }
+    for (int i = 0; i < kSegs; ++i) mbar_init(bar(kSegFull + i), 1);
     mbar_init(bar(kQFull), 256);
     mbar_init(bar(kSFull0), 1);
     mbar_init(bar(kSFull1), 1);
@@ -206,16 +220,34 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
   // schedule (unless entries were evicted) and the first q^ are made while the
   // preceding kernel finishes.
   if (a.drop != nullptr) pdl_wait();
+  PagedRange* s_range = reinterpret_cast<PagedRange*>(smem + kOffMisc + 16);
+  PagedSegment* segs = reinterpret_cast<PagedSegment*>(smem + kOffSeg);
+  PagedSegment sg;
   if (warp == 0) {
-    const PagedRange r = paged_range(a, blockIdx.x, kKT);
-    if (lane == 0) *s_range = r;
+    PagedRange r = paged_range(a, blockIdx.x, kKT);
+    if (!paged_next(a, r, sg, kKT)) sg.n_tiles = 0;
+    if (lane == 0) {
+      *s_range = r;
+      segs[0] = sg;
+    }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  PagedRange walk = *s_range;
-  PagedSegment sg;
+  uint32_t seg = 0;
+  auto wait = [&](int b, uint32_t parity) {
+    if (!mbar_test(bar(b), parity)) mbar_wait(bar(b), parity, abort_flag, err);
+  };
+  // the next segment, as the address warps found it
+  auto next_seg = [&]() {
+    if (seg > 0) {  // (the first is there)
+      wait(kSegFull + seg % kSegs, (seg / kSegs - (seg % kSegs == 0)) & 1u);
+      if (*abort_flag) return false;
+    }
+    sg = segs[seg++ % kSegs];
+    return sg.n_tiles > 0;
+  };
 
   if (warp < 8) {
     // =================== q^, softmax, epilogue ===================
@@ -229,8 +261,26 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
     const int R = a.R;
     uint32_t gt = 0;
     int4 cut = make_int4(-1, 0, 0, 0);
-    bool waited = false;
-    while (paged_next(a, walk, sg, kKT)) {
+    uint4 va[8], vb[8];
+    float snk = 0.f;
+    auto load_q = [&]() {  // of the next segment
+      const int nh = min(kH, a.H - sg.g * kH);
+      const uint16_t* qrow = a.q + ((int64_t)sg.b * a.H + sg.g * kH) * kD + 8 * lane;
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const int h = warp + 8 * u;
+        va[u] = vb[u] = make_uint4(0, 0, 0, 0);
+        if (h < nh) {
+          va[u] = *reinterpret_cast<const uint4*>(qrow + h * kD);
+          vb[u] = *reinterpret_cast<const uint4*>(qrow + h * kD + 256);
+        }
+      }
+      if (st < nh) snk = a.sink[sg.g * kH + st];
+    };
+    reinterpret_cast<float2*>(g_s)[st] = reinterpret_cast<const float2*>(a.q_norm_g)[st];
+    bool more = next_seg();
+    if (more) load_q();
+    while (more) {
       const int nh = min(kH, a.H - sg.g * kH);
       const int64_t head0 = (int64_t)sg.b * a.H + sg.g * kH;
       if (sg.cut_last >= 0) cut = make_int4(sg.item, sg.cut_last, sg.slot, 0);
@@ -238,27 +288,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
       // the K-major operand layout: warp w takes heads w, w + 8, ..., lane l
       // dims 8l .. 8l+7 and 256+8l ..; heads that the group does not have are
       // 0.  Four heads' loads at a time.
-      uint4 va[4], vb[4];
-      auto load_q = [&](int half) {
-        const uint16_t* qrow = a.q + head0 * kD + 8 * lane;
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const int h = warp + 8 * (4 * half + u);
-          va[u] = vb[u] = make_uint4(0, 0, 0, 0);
-          if (h < nh) {
-            va[u] = *reinterpret_cast<const uint4*>(qrow + h * kD);
-            vb[u] = *reinterpret_cast<const uint4*>(qrow + h * kD + 256);
-          }
-        }
-      };
-      load_q(0);
       if (st < R / 2) {
         float cs, sn;
         rope_cos_sin(sg.seq.pos, a.rope.t[st], &cs, &sn);
         rope_s[st] = make_float2(cs, sn);
       }
       if (st < kH) {
-        sink_s[st] = st < nh ? a.sink[sg.g * kH + st] * kLog2e : 0.f;
+        sink_s[st] = st < nh ? snk * kLog2e : 0.f;
         mrun[st] = kNoRef;
       }
       named_bar(1, 256);
@@ -266,8 +302,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
         float2 g[8], rope[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          g[k] = *reinterpret_cast<const float2*>(a.q_norm_g + 8 * lane + 2 * k);
-          g[4 + k] = *reinterpret_cast<const float2*>(a.q_norm_g + 256 + 8 * lane + 2 * k);
+          g[k] = *reinterpret_cast<const float2*>(g_s + 8 * lane + 2 * k);
+          g[4 + k] = *reinterpret_cast<const float2*>(g_s + 256 + 8 * lane + 2 * k);
           const int d = 256 + 8 * lane + 2 * k - (kD - R);
           rope[k] = d >= 0 ? rope_s[d >> 1] : make_float2(1.f, 0.f);
         }
@@ -301,19 +337,22 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
             st_shared16(q_base + offA + sw, pq[0], pq[1], pq[2], pq[3]);
             st_shared16(q_base + offB + sw, pq[4], pq[5], pq[6], pq[7]);
           }
-          if (half == 0) load_q(1);
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            va[u] = va[u + 4];
+            vb[u] = vb[u + 4];
+          }
         }
       }
       fence_async_smem();
       mbar_arrive(bar(kQFull));
-      if (!waited) pdl_wait();
-      waited = true;
+      if (gt == 0) pdl_wait();
       float lpart[8];  // columns col0, + 1 of each 8, both keys
 #pragma unroll
       for (int i = 0; i < 8; ++i) lpart[i] = 0.f;
-      for (int tile = 0; tile < sg.n_tiles; ++tile, ++gt) {
-        mbar_wait(bar(kSFull0 + (gt & 1u)), (gt >> 1) & 1u, abort_flag, err);
-        mbar_wait(bar(kRowFull + gt % kAhead), (gt / kAhead) & 1u, abort_flag, err);  // (the tile's addresses)
+      for (int tile = 0; tile < sg.n_tiles; ++tile) {
+        wait(kSFull0 + (gt & 1u), (gt >> 1) & 1u);
+        wait(kRowFull + gt % kAhead, (gt / kAhead) & 1u);  // (the tile's addresses)
         tc_fence_after();
         float z[16];
         tmem_ld_16x32(t_lane + (gt & 1u) * 64u + (uint32_t)h0, z);
@@ -387,7 +426,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
         }
         if (tile > 0) {
           // the previous tile's PV must be done before P^T and O^T change
-          mbar_wait(bar(kPVDone), (gt - 1) & 1u, abort_flag, err);
+          wait(kPVDone, (gt - 1) & 1u);
           tc_fence_after();
         }
         // heads h0 + 8j .. + 7 are the 16-byte piece 4 hf + j of the key's row
@@ -422,10 +461,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
         fence_async_smem();
         tc_fence_before();
         mbar_arrive(bar(kPFull));
+        ++gt;
       }
       // ---------------- epilogue ----------------
-      mbar_wait(bar(kPVDone), (gt - 1) & 1u, abort_flag, err);
-      tc_fence_after();
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         float a0 = lpart[2 * j], a1 = lpart[2 * j + 1];
@@ -450,7 +488,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
         }
       }
       named_bar(1, 256);
-      const bool odd = r & 1;
+      wait(kPVDone, (gt - 1) & 1u);
+      tc_fence_after();
 #pragma unroll 1
       for (int c = 0; c < 4; ++c) {
         const int d = 128 * c + r;
@@ -458,28 +497,27 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
         tmem_ld32(t_lane + 128u + 64u * c + (uint32_t)h0, v);
         tmem_ld_wait();
         if (sg.whole) {
-          // lanes r and r^1 hold dims d and d^1: one exchange per head pair
-          // gives the even lane both dims of the even head and the odd lane
-          // both dims of the odd head, so each lane rotates its pair (rope
-          // slice, by -pos) and writes one 4-byte word of the stage
-          const bool rot = d >= kD - R;
-          float cs = 1.f, sn = 0.f;
-          if (rot) {
-            cs = rope_s[(d - (kD - R)) >> 1].x;
-            sn = rope_s[(d - (kD - R)) >> 1].y;
-          }
-          const uint32_t dd = (uint32_t)(d & ~1) * 2u;
+          if (128 * c + 32 * q4 + 31 >= kD - R) {
+            // the rope slice, rotated by -pos: lanes r and r^1 hold dims d and
+            // d^1 (x0 cs + x1 sn, -x0 sn + x1 cs)
+            float cs = 1.f, sn = 0.f;
+            if (d >= kD - R) {
+              cs = rope_s[(d - (kD - R)) >> 1].x;
+              sn = rope_s[(d - (kD - R)) >> 1].y;
+              if (r & 1) sn = -sn;
+            }
 #pragma unroll
-          for (int i = 0; i < 32; i += 2) {
-            const float got = __shfl_xor_sync(0xffffffffu, odd ? v[i] : v[i + 1], 1);
-            const int h = h0 + i + (odd ? 1 : 0);
-            const float s = inv_s[h];
-            float2 x = mul_f2(make_float2(odd ? got : v[i], odd ? v[i + 1] : got), make_float2(s, s));
-            if (rot)  // (x0 cs + x1 sn, -x0 sn + x1 cs)
-              x = fma_f2(make_float2(x.x, x.x), make_float2(cs, -sn), mul_f2(make_float2(x.y, x.y), make_float2(sn, cs)));
-            st_shared32(q_base + (uint32_t)h * kStagePitch + dd, f2_to_bf2x2(x.x, x.y));
+            for (int i = 0; i < 32; ++i) v[i] = v[i] * cs + __shfl_xor_sync(0xffffffffu, v[i], 1) * sn;
           }
-        } else if (walk.kind == 0) {  // through the ring, which this only segment has left
+          const float4* inv4 = reinterpret_cast<const float4*>(inv_s + h0);
+          const uint32_t at = q_base + (uint32_t)h0 * kStagePitch + 2u * (uint32_t)d;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float4 s4 = inv4[i];
+            st_shared_halves<kStagePitch>(at + 4u * i * kStagePitch, f2_to_bf2x2(v[4 * i] * s4.x, v[4 * i + 1] * s4.y));
+            st_shared_halves<kStagePitch>(at + (4u * i + 2u) * kStagePitch, f2_to_bf2x2(v[4 * i + 2] * s4.z, v[4 * i + 3] * s4.w));
+          }
+        } else if (sg.alone) {  // through the ring, which this only segment has left
 #pragma unroll
           for (int i = 0; i < 32; ++i) st_shared32(kv_base + (uint32_t)((h0 + i) * kD + d) * 4u, __float_as_uint(v[i]));
         } else {
@@ -487,7 +525,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
           for (int i = 0; i < 32; ++i) part[2 * kH + (h0 + i) * kD + d] = v[i];
         }
       }
-      if (!sg.whole && walk.kind == 0) {
+      if (!sg.whole && sg.alone) {
         fence_async_smem();
         named_bar(1, 256);
         if (st < 8) {
@@ -497,23 +535,25 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
       }
       tc_fence_before();
       mbar_arrive(bar(kEpiDone));
-      if (sg.whole) {
+      const bool staged = sg.whole;
+      if (staged) {
         fence_async_smem();
         named_bar(1, 256);
         if (st < nh) {
           bulk_s2g(a.out + (head0 + st) * kD, q_base + (uint32_t)st * kStagePitch, kD * 2);
           bulk_commit();
-          bulk_wait_read0();  // the stage is read before the next segment's q^ goes in
         }
       }
+      more = !sg.alone && next_seg();
+      if (more) load_q();
+      if (staged && st < kH) bulk_wait_read0();  // the stage is read before the next segment's q^ goes in
       named_bar(1, 256);
     }
-    if (!waited) pdl_wait();
+    pdl_wait();
     if (st == 0) a.cut[blockIdx.x] = cut;
     if (st < kH) bulk_wait0();
   } else if (warp == kMmaWarp) {
     // =================== MMA issuer ===================
-    pdl_wait();
     // low words of the descriptors; the strides between 8-row groups, the
     // swizzle and the rest of the high words are the same
     const uint32_t qk_a = (uint32_t)sdesc_sw128(kv_base, 16, 1024), qk_b = (uint32_t)sdesc_sw128(q_base, 16, 1024);
@@ -524,66 +564,76 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
     // cycles, what its 6 KiB of shared memory take; from a branch of one lane
     // it was 54 to 90.
     uint32_t gt = 0, active = 0;
+    uint32_t qs = 0, qph = 0, ps = 0;  // slot and phase of the next chunk of the first product, slot of the second's
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-    while (__any_sync(0xffffffffu, paged_next(a, walk, sg, kKT))) {
-      const int n_tiles = __shfl_sync(0xffffffffu, sg.n_tiles, 0);
-      auto qk_chunk = [&](uint32_t g, int c) {
-        const uint32_t slot = (4 * g + c) % kSlots;
-        mma_qk_chunk(tm + (g & 1u) * 64u, qk_a + ((slot * kSlot) >> 4), qk_b + ((2u * c * 8192u) >> 4), sd_hi, kIdescQK, c);
-      };
-      auto kv_full = [&](uint32_t g, int c) { return bar(kKVFull + (4 * g + c) % kSlots); };
-      auto kv_phase = [&](uint32_t g, int c) { return ((4 * g + c) / kSlots) & 1u; };
-      mbar_wait(bar(kQFull), active & 1u, abort_flag, err);
-      tc_fence_after();
-      int qc = 0;  // chunks of the tile's first product that are issued
-      for (int tile = 0; tile < n_tiles; ++tile, ++gt) {
-        if (qc < 4) {
-          for (; qc < 4; ++qc) {
-            mbar_wait(kv_full(gt, qc), kv_phase(gt, qc), abort_flag, err);
+    // (The first pass is dry: nothing is issued and nothing waits, but the code
+    // comes in while the schedule is made; on a busy memory its first pass
+    // waits 2 to 3 us for instructions.)
+    for (uint32_t go = 0;; go = 1) {
+      if (go && !__any_sync(0xffffffffu, next_seg())) break;
+      const int n_tiles = go ? __shfl_sync(0xffffffffu, sg.n_tiles, 0) : 1;
+      int qc = 0;  // half tiles whose first product is issued
+      if (go) wait(kQFull, active & 1u);
+      for (int tile = 0; tile < n_tiles; ++tile) {
+        const int now = 2 * (tile + 1), end = go ? 2 * min(tile + 2, n_tiles) : 1;
+        // the tile's first product, and until P^T comes the next tile's, as it
+        // arrives, two chunks at a time (asking costs as much as four MMAs;
+        // chunks become full in order, so the second stands for both)
+        int q = qc;
+        while (q < end) {
+          const uint32_t s1 = qs + 1 == kSlots ? 0u : qs + 1, ph1 = s1 == 0 ? qph ^ 1u : qph;
+          const uint32_t t = gt + (q >= now ? 1u : 0u);
+          if (go) {
+            if (q < now) {
+              wait(kKVFull + s1, ph1);
+            } else if (!__all_sync(0xffffffffu, mbar_test(bar(kKVFull + s1), ph1))) {
+              if (__any_sync(0xffffffffu, mbar_test(bar(kPFull), gt & 1u) || *abort_flag)) break;
+              continue;
+            }
             __syncwarp();
             tc_fence_after();
-            qk_chunk(gt, qc);
           }
-          mma_commit_elect(bar(kSFull0 + (gt & 1u)));
-        }
-        // until P^T comes: the next tile's first product, as it arrives
-        qc = 0;
-        const bool more = tile + 1 < n_tiles;
-        while (more && qc < 4) {
-          const bool p_here = mbar_test(bar(kPFull), gt & 1u) || *abort_flag;
-          const bool kv_here = mbar_test(kv_full(gt + 1, qc), kv_phase(gt + 1, qc));
-          if (__all_sync(0xffffffffu, kv_here)) {
-            tc_fence_after();
-            qk_chunk(gt + 1, qc);
-            if (++qc == 4) mma_commit_elect(bar(kSFull0 + ((gt + 1) & 1u)));
-          } else if (__any_sync(0xffffffffu, p_here)) {
-            break;
+          const uint32_t d_s = tm + (t & 1u) * 64u, db = qk_b + ((q & 1u) ? 2048u : 0u);
+          mma_qk_chunk(d_s, qk_a + qs * (kSlot >> 4), db, sd_hi, kIdescQK, q & 1, go);
+          mma_qk_chunk(d_s, qk_a + s1 * (kSlot >> 4), db + 1024u, sd_hi, kIdescQK, 1, go);
+          mma_commit_elect(bar(kSFull0 + (t & 1u)), go & q);
+          if (go) {
+            qph = s1 + 1 == kSlots ? ph1 ^ 1u : ph1;
+            qs = s1 + 1 == kSlots ? 0u : s1 + 1;
           }
+          ++q;
         }
-        mbar_wait(bar(kPFull), gt & 1u, abort_flag, err);
-        if (tile == 0 && active > 0) mbar_wait(bar(kEpiDone), (active - 1) & 1u, abort_flag, err);
-        __syncwarp();
-        tc_fence_after();
-        if (a.weights && lane == 0) {  // P^T as it lies, for the weights
-          bulk_s2g(a.tile_p + ((int64_t)sg.item * a.item_tiles + sg.tile0 + tile) * kKT * kH, p_base, kKT * kH * 2);
-          bulk_commit();
+        if (go) {
+          qc = q;
+          wait(kPFull, gt & 1u);
+          if (tile == 0 && active > 0) wait(kEpiDone, (active - 1) & 1u);
+          __syncwarp();
+          tc_fence_after();
+          if (a.weights && lane == 0) {  // P^T as it lies, for the weights
+            bulk_s2g(a.tile_p + ((int64_t)sg.item * a.item_tiles + sg.tile0 + tile) * kKT * kH, p_base, kKT * kH * 2);
+            bulk_commit();
+          }
+          __syncwarp();
         }
-        __syncwarp();
         const uint32_t acc0 = tile == 0 ? 0u : 1u;
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          const uint32_t slot = (4 * gt + c) % kSlots;
-          mma_pv_chunk(tm + 128u + 64u * c, pv_a + ((slot * kSlot) >> 4), pv_b, sd_hi, kIdescPV, acc0);
-          mma_commit_elect(bar(kKVEmpty + slot));
+          mma_pv_chunk(tm + 128u + 64u * c, pv_a + ps * (kSlot >> 4), pv_b, sd_hi, kIdescPV, acc0, go);
+          mma_commit_elect(bar(kKVEmpty + ps), go);
+          ps += go;
+          if (ps == kSlots) ps = 0;
         }
-        if (a.weights) {
+        if (go && a.weights) {
           if (lane == 0) bulk_wait_read0();  // before P^T changes
           __syncwarp();
         }
-        mma_commit_elect(bar(kPVDone));
+        mma_commit_elect(bar(kPVDone), go);
+        if (!go) pdl_wait();
+        gt += go;
       }
-      ++active;
+      active += go;
     }
+    pdl_wait();
     // drain: every MMA issued has finished before the block exits
     mma_commit_elect(bar(kDrain));
     mbar_wait(bar(kDrain), 0, abort_flag, err);
@@ -593,10 +643,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
     // =================== row addresses ===================
     // (positions and the table are inputs; the listed slots a kernel may have
     // just written)
-    if (a.sparse) pdl_wait();
     const int key = tid - kPtr0;  // 0..63
     uint32_t gt = 0;
-    while (paged_next(a, walk, sg, kKT)) {
+    PagedRange walk = *s_range;
+    sg = segs[0];
+    bool more = sg.n_tiles > 0;
+    while (more) {
+      if (a.sparse && gt == 0) pdl_wait();
       // the segment's query into L2 as well, a head a thread
       if (key < min(kH, a.H - sg.g * kH)) prefetch_l2_bulk(a.q + ((int64_t)sg.b * a.H + sg.g * kH + key) * kD, kD * 2u);
       for (int tile = 0; tile < sg.n_tiles; ++tile, ++gt) {
@@ -604,9 +657,16 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
         bool fp8 = false;
         const uint8_t* row = j < sg.seq.n_keys ? paged_key(a, sg.b, sg.seq, j, &fp8) : nullptr;
         if (row) prefetch_l2_bulk(row, fp8 ? (uint32_t)a.row_bytes : kD * 2u);
-        if (gt >= kAhead) mbar_wait(bar(kRowEmpty + gt % kAhead), (gt / kAhead - 1) & 1u, abort_flag, err);
+        if (gt >= kAhead) wait(kRowEmpty + gt % kAhead, (gt / kAhead - 1) & 1u);
         rows[(gt % kAhead) * kKT + key] = reinterpret_cast<unsigned long long>(row) | (fp8 ? 1ull : 0ull);
         mbar_arrive(bar(kRowFull + gt % kAhead));
+      }
+      more = paged_next(a, walk, sg, kKT);
+      ++seg;
+      if (key == 0) {
+        if (!more) sg.n_tiles = 0;
+        segs[seg % kSegs] = sg;
+        mbar_arrive(bar(kSegFull + seg % kSegs));
       }
     }
   } else if (warp != kFenceWarp) {
@@ -616,14 +676,14 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
     int left = 0;               // tiles of the segment
     auto next_tile = [&]() {
       if (left == 0) {
-        if (!paged_next(a, walk, sg, kKT)) return false;
+        if (!next_seg()) return false;
         left = sg.n_tiles;
       }
       --left;
       return true;
     };
     auto acquire = [&](uint32_t u) {  // chunk u's slot
-      if (u >= kSlots) mbar_wait(bar(kKVEmpty + u % kSlots), (u / kSlots - 1) & 1u, abort_flag, err);
+      if (u >= kSlots) wait(kKVEmpty + u % kSlots, (u / kSlots - 1) & 1u);
     };
     if (!kFp8) {
       // a thread takes the 16-byte piece pt % 16 of four rows' 256 bytes; a
@@ -634,7 +694,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
       const uint32_t at = (uint32_t)(piece >> 3) * kBlk + sw128(row0, piece & 7);
       for (uint32_t gt = 0; next_tile(); ++gt) {
         const uint32_t rs = gt % kAhead;
-        mbar_wait(bar(kRowFull + rs), (gt / kAhead) & 1u, abort_flag, err);
+        wait(kRowFull + rs, (gt / kAhead) & 1u);
         const uint16_t* src[kN];
         uint32_t bytes[kN];
 #pragma unroll
@@ -666,7 +726,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
       uint32_t sc[kN];
       auto load = [&](uint32_t gt) {
         const uint32_t rs = gt % kAhead;
-        mbar_wait(bar(kRowFull + rs), (gt / kAhead) & 1u, abort_flag, err);
+        wait(kRowFull + rs, (gt / kAhead) & 1u);
         if (rope) return;
 #pragma unroll
         for (int i = 0; i < kN; ++i) {
@@ -720,9 +780,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
     // The rows are written in the generic proxy.  The fence between the proxies
     // costs 0.2 us a chunk in the issuing warp; here it is off its path.
     uint32_t u = 0;
-    while (paged_next(a, walk, sg, kKT)) {
+    while (next_seg()) {
       for (int i = 4 * sg.n_tiles; i > 0; --i, ++u) {
-        mbar_wait(bar(kKVLanded + u % kSlots), (u / kSlots) & 1u, abort_flag, err);
+        wait(kKVLanded + u % kSlots, (u / kSlots) & 1u);
         fence_async_smem();
         if (lane == 0) mbar_arrive(bar(kKVFull + u % kSlots));
       }
