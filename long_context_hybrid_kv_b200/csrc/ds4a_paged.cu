@@ -34,9 +34,10 @@ __global__ void __launch_bounds__(kGenThreads) paged_attend_generic_kernel(const
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pdl_trigger();
   pdl_wait();
-  if (warp == 0) {
-    const PagedRange r = paged_range(a, blockIdx.x, kGenKeys);
-    if (lane == 0) s_r = r;
+  {
+    __shared__ int s_n[512], s_fit[32];
+    const PagedRange r = paged_range(a, blockIdx.x, kGenKeys, s_n, 512, s_fit);
+    if (tid == 0) s_r = r;
   }
   __syncthreads();
   const PagedRange r = s_r;

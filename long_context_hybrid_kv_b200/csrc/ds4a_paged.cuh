@@ -126,7 +126,6 @@ __device__ __forceinline__ int paged_item_seq(const PagedArgs& a, int item) {
 constexpr int kPagedWhole = 4, kPagedLeast = 2;
 constexpr int kPagedCost = 6;  // of a segment besides its tiles, in tiles (measured: 14 us a second segment)
 constexpr int kPagedJoin = 4;  // of the joining, in tiles
-constexpr int kPagedChunks = 8;  // of 32 sequences, that a warp holds in registers (296 blocks at most)
 
 // More items than blocks: the blocks that take part, where block c's range
 // begins before its ends are moved, and the block that holds tile t.
@@ -140,7 +139,7 @@ __device__ __forceinline__ int paged_block_of(int t, int total, int ge) {
   return (unsigned)t < wide ? (int)((unsigned)t / (q + 1)) : (int)(rem + ((unsigned)t - wide) / q);
 }
 
-// A block's place in the schedule, found by one warp (all 32 lanes).
+// A block's place in the schedule.
 struct PagedRange {
   int kind;           // 0: a piece of an item, 1: whole items that share the block, 2: a range of the row of all tiles
   int item;           // the first
@@ -149,14 +148,25 @@ struct PagedRange {
   int T, stop, done;  // 1: items above T / 2 are left out; twice the cost at which to stop, cost before the first
   int item_t0, raw0, total, ge;  // 2: tiles before the first item, start before moving, tiles and blocks in all
 };
-__device__ __forceinline__ PagedRange paged_range(const PagedArgs& a, int c, int kt) {
-  const int lane = threadIdx.x & 31, hg = a.hgroups, items = a.B * hg;
-  auto tiles_at = [&](int b0) {
-    const int b = b0 + lane;
-    if (b >= a.B) return 0;
+
+// Found by the whole block, the result valid in its warp 0.  s_n: room for
+// `staged` lengths (at least the number of blocks), s_fit: 32 ints.  It stands
+// before the first product of every launch, so it is short: all lengths are
+// fetched at once, T is searched by up to 16 warps side by side, and no loop
+// is unrolled (at a first pass instructions cost more than their work).
+__device__ __forceinline__ PagedRange paged_range(const PagedArgs& a, int c, int kt, int* s_n, int staged, int* s_fit) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, hg = a.hgroups, items = a.B * hg;
+  auto tiles_of = [&](int b) {
     const PagedSeq s = paged_seq(a, b);
     if (s.pos < 0 && c == 0) raise_err(a.err, DS4A_DEV_BAD_POS);
     return paged_tiles(s, kt);
+  };
+#pragma unroll 1
+  for (int b = tid; b < min(a.B, staged); b += blockDim.x) s_n[b] = tiles_of(b);
+  __syncthreads();
+  auto tiles_at = [&](int b0) {  // of sequence b0 + lane
+    const int b = b0 + lane;
+    return b >= a.B ? 0 : b < staged ? s_n[b] : tiles_of(b);
   };
   auto scan = [&](int v) {
 #pragma unroll
@@ -166,123 +176,116 @@ __device__ __forceinline__ PagedRange paged_range(const PagedArgs& a, int c, int
     }
     return v;
   };
-  auto sum = [&](int v) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    return v;
-  };
   PagedRange r;
   r.kind = 1;
   r.item = items;  // nothing to do
   r.t0 = r.t1 = r.last = r.T = r.stop = r.done = r.item_t0 = r.raw0 = r.total = r.ge = 0;
-  int total = 0;
+  if (items > a.G && warp > 0) return r;
+  int total = 0, most = 0, some = 0;  // tiles, the longest item's, items that have any
+#pragma unroll 1
+  for (int b0 = 0; b0 < a.B; b0 += 32) {
+    const int v = tiles_at(b0);
+    total += v;
+    most = max(most, v);
+    some += v > 0;
+  }
+  total = __reduce_add_sync(0xffffffffu, total) * hg;
+  some = __reduce_add_sync(0xffffffffu, some) * hg;
+  most = __reduce_max_sync(0xffffffffu, most);
   bool rows = false;
   if (items <= a.G) {
-    int n[kPagedChunks], most = 0;
-#pragma unroll
-    for (int k = 0; k < kPagedChunks; ++k) {
-      n[k] = 0;
-      if (32 * k >= a.B) break;
-      n[k] = tiles_at(32 * k);
-      total += n[k] * hg;
-      most = max(most, n[k]);
-    }
-    total = sum(total);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
-    int T = 0;
+    int T = 0, big = 0;
     auto pieces = [&](int v) {  // 0: none, or small
       return 2 * v <= T ? 0 : v <= kPagedWhole ? 1 : (int)((unsigned)(v + T - 1) / (unsigned)T);
     };
     auto cost = [&](int v) { return v > 0 && 2 * v <= T ? v + kPagedCost : 0; };
-    int big = 0, small = 0;
     auto fits = [&](int t) {
       T = t;
-      big = small = 0;
-#pragma unroll
-      for (int k = 0; k < kPagedChunks; ++k) {
-        if (32 * k >= a.B) break;
-        big += pieces(n[k]) * hg;
-        small += cost(n[k]) * hg;
+      big = 0;
+      int small = 0;
+#pragma unroll 1
+      for (int b0 = 0; b0 < a.B; b0 += 32) {
+        const int v = tiles_at(b0);
+        big += pieces(v);
+        small += cost(v);
       }
-      big = sum(big);
-      small = sum(small);
+      big = __reduce_add_sync(0xffffffffu, big) * hg;
+      small = __reduce_add_sync(0xffffffffu, small) * hg;
       return big + (small + T + kPagedCost - 1) / (T + kPagedCost) <= a.G;
     };
-    // (T = the longest item's tiles fits: one block an item or fewer)
-    int yes = max(kPagedLeast, (total + a.G - 1) / a.G);
-    if (!fits(yes)) {
-      int no = yes;  // (sum n / T + 1 over the items bounds the pieces)
-      yes = max(no + 1, a.G > items ? min(most, (total + a.G - items - 1) / (a.G - items)) : most);
-      if (!fits(yes)) yes = max(most, yes);  // (an item a block, or fewer blocks)
+    // T = the longest item's tiles fits: one block an item or fewer.  (The sum
+    // of n / T + 1 over the items bounds the pieces: look up to there first.)
+    const int lo = max(kPagedLeast, (total + a.G - 1) / a.G), nc = min(16, (int)blockDim.x >> 5);
+    int no = lo - 1, yes = max(most, lo);
+    int top = a.G > items ? max(lo, min(yes, (total + a.G - items - 1) / (a.G - items))) : yes;
 #pragma unroll 1
-      while (yes - no > 1) {
-        const int mid = (yes + no) >> 1;
-        if (fits(mid)) yes = mid;
-        else no = mid;
+    while (yes - no > 1) {
+      auto cand = [&](int w) { return no + 1 + (int)((int64_t)(top - no - 1) * w / (nc - 1)); };
+      if (warp < nc) {
+        const bool f = fits(cand(warp));
+        if (lane == 0) s_fit[warp] = f;
       }
-      fits(yes);
+      __syncthreads();
+      const unsigned int m = __ballot_sync(0xffffffffu, lane < nc && s_fit[lane] != 0);
+      if (m == 0) {
+        no = top;
+      } else {
+        const int w = __ffs(m) - 1, hi = cand(w);
+        if (w > 0) no = cand(w - 1);
+        yes = hi;
+      }
+      top = yes;
+      __syncthreads();
     }
+    if (warp > 0) return r;
+    fits(yes);
     // (lengths that do not fit well: the row of tiles is better, although its
     // blocks have two segments)
     rows = T > (total + a.G - 1) / a.G + kPagedCost && most > kPagedWhole;
-    int blocks = 0, before = 0;
-    const int share = T + kPagedCost, s0 = (c - big) * 2 * share;  // a shared block takes the items whose middle lies in its share
-    r.T = T;
-    r.stop = s0 + 2 * share;
-    bool found = false;
-#pragma unroll
-    for (int k = 0; k < kPagedChunks; ++k) {
-      if (32 * k >= a.B || rows) break;
-      const int p = pieces(n[k]) * hg, w = cost(n[k]);
-      if (c < big) {
-        const int pi = scan(p);
-        const unsigned int here = __ballot_sync(0xffffffffu, blocks + pi > c);
-        if (here && !found) {
-          found = true;
-          const int l = __ffs(here) - 1;
-          const int n_l = __shfl_sync(0xffffffffu, n[k], l), p_l = __shfl_sync(0xffffffffu, p, l) / hg;
-          const int at = c - blocks - __shfl_sync(0xffffffffu, pi - p, l), g = at / p_l, j = at - g * p_l;
-          r.kind = 0;
-          r.item = (32 * k + l) * hg + g;
-          r.t0 = (int)((unsigned)(j * n_l) / (unsigned)p_l);
-          r.t1 = (int)((unsigned)((j + 1) * n_l) / (unsigned)p_l);
-          r.last = c - j + p_l - 1;
+    if (!rows) {
+      int blocks = 0, before = 0;
+      const int share = T + kPagedCost, s0 = (c - big) * 2 * share;  // a shared block takes the items whose middle lies in its share
+      r.T = T;
+      r.stop = s0 + 2 * share;
+#pragma unroll 1
+      for (int b0 = 0; b0 < a.B; b0 += 32) {
+        const int n = tiles_at(b0);
+        if (c < big) {
+          const int p = pieces(n) * hg, pi = scan(p);
+          const unsigned int here = __ballot_sync(0xffffffffu, blocks + pi > c);
+          if (here) {
+            const int l = __ffs(here) - 1;
+            const int n_l = __shfl_sync(0xffffffffu, n, l), p_l = __shfl_sync(0xffffffffu, p, l) / hg;
+            const int at = c - blocks - __shfl_sync(0xffffffffu, pi - p, l), g = at / p_l, j = at - g * p_l;
+            r.kind = 0;
+            r.item = (b0 + l) * hg + g;
+            r.t0 = (int)((unsigned)(j * n_l) / (unsigned)p_l);
+            r.t1 = (int)((unsigned)((j + 1) * n_l) / (unsigned)p_l);
+            r.last = c - j + p_l - 1;
+            break;
+          }
+          blocks += __shfl_sync(0xffffffffu, pi, 31);
+        } else {
+          const int w = cost(n), wi = scan(w * hg);
+          // the sequence's last group lies behind the share's begin
+          const unsigned int here = __ballot_sync(0xffffffffu, w > 0 && 2 * (before + wi) - w >= s0);
+          if (here) {
+            const int l = __ffs(here) - 1;
+            int g = 0, d = before + __shfl_sync(0xffffffffu, wi - w * hg, l);
+            const int w_l = __shfl_sync(0xffffffffu, w, l);
+            for (; 2 * d + w_l < s0; d += w_l) ++g;
+            r.item = (b0 + l) * hg + g;
+            r.done = d;
+            break;
+          }
+          before += __shfl_sync(0xffffffffu, wi, 31);
         }
-        blocks += __shfl_sync(0xffffffffu, pi, 31);
-      } else {
-        const int wi = scan(w * hg);
-        // the sequence's last group lies behind the share's begin
-        const int end2 = 2 * (before + wi) - w;
-        const unsigned int here = __ballot_sync(0xffffffffu, w > 0 && end2 >= s0);
-        if (here && !found) {
-          found = true;
-          const int l = __ffs(here) - 1;
-          int g = 0, d = before + __shfl_sync(0xffffffffu, wi - w * hg, l);
-          const int w_l = __shfl_sync(0xffffffffu, w, l);
-          for (; 2 * d + w_l < s0; d += w_l) ++g;
-          r.item = (32 * k + l) * hg + g;
-          r.done = d;
-        }
-        before += __shfl_sync(0xffffffffu, wi, 31);
       }
+      return r;
     }
-    if (!rows) return r;
   }
   int v = 0, inc = 0;
   if (items > a.G) {
-    int most = 0, some = 0;  // longest item, items with tiles
-#pragma unroll 1
-    for (int b0 = 0; b0 < a.B; b0 += 32) {
-      v = tiles_at(b0);
-      total += v;
-      most = max(most, v);
-      some += v > 0;
-    }
-    total = sum(total) * hg;
-    some = sum(some) * hg;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
     const int64_t costs = (int64_t)total + (int64_t)some * kPagedCost;
     const int share = (int)((costs + a.G - 1) / a.G), longest = most + kPagedCost;
     // with items that are long next to a share, as many of the longest as one takes

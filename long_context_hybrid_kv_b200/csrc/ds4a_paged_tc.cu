@@ -43,6 +43,9 @@ constexpr int kFenceWarp = 19;
 constexpr int kSlots = 9;             // ring of 128-dim chunks
 constexpr int kAhead = 4;             // tiles of row addresses
 constexpr int kSegs = 8;              // segments made known: the address warps are at most five tiles, so segments, ahead of the rest
+// cos, sin and sinks of four segments: while one is in its epilogue the ring
+// can hold the next two's rows and the first of the third's
+constexpr int kTabs = 4;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kRescaleLog2 = 8.0f;  // O^T is rescaled when a head's maximum grows by more than 2^8
 constexpr float kNoRef = -1e30f;      // reference of a head that has seen no key: finite, below any logit
@@ -53,7 +56,7 @@ constexpr uint32_t kOffKV = 0;
 constexpr uint32_t kOffQ = kSlots * kSlot;       // 8 blocks x [64 heads][128 B]
 constexpr uint32_t kOffP = kOffQ + 65536;        // [64 keys][128 B]
 constexpr uint32_t kOffBar = kOffP + kBlk;
-constexpr uint32_t kOffSeg = kOffBar + 448;         // segments
+constexpr uint32_t kOffSeg = kOffBar + 480;         // segments
 constexpr uint32_t kOffMisc = kOffSeg + kSegs * 64;     // abort flag, TMEM address, the block's range
 constexpr uint32_t kOffRow = kOffMisc + 128;      // [4 tiles][64] row addresses, bit 0: FP8
 constexpr uint32_t kOffRed = kOffRow + kAhead * kKT * 8;  // [4][64] floats
@@ -61,9 +64,8 @@ constexpr uint32_t kOffMrun = kOffRed + 1024;
 constexpr uint32_t kOffAlpha = kOffMrun + 256;
 constexpr uint32_t kOffInv = kOffAlpha + 256;
 constexpr uint32_t kOffSink = kOffInv + 256;
-constexpr uint32_t kOffRope = kOffSink + 256;    // [128] (cos, sin) of the segment's position
-constexpr uint32_t kOffG = kOffRope + 1024;  // [512] norm weights
-constexpr uint32_t kSmemBytes = kOffG + 2048 + 1024;
+constexpr uint32_t kOffRope = kOffSink + kTabs * 256;  // [4 segments][128] (cos, sin) of the position
+constexpr uint32_t kSmemBytes = kOffRope + kTabs * 1024 + 1024;
 static_assert(kSmemBytes <= 232448, "shared memory of a block");
 // The finished output goes out through the q^ and P^T buffers, a head's 1024
 // bytes 1088 apart (the two heads that a warp writes at a time then lie in
@@ -73,9 +75,9 @@ static_assert(kH * kStagePitch <= 65536 + kBlk && kH * kD * 4 <= kSlots * kSlot,
 
 enum Bar {
   kKVLanded = 0, kKVFull = kKVLanded + kSlots, kKVEmpty = kKVFull + kSlots, kRowFull = kKVEmpty + kSlots, kRowEmpty = kRowFull + kAhead,
-  kSegFull = kRowEmpty + kAhead, kQFull = kSegFull + kSegs, kSFull0, kSFull1, kPFull, kPVDone, kEpiDone, kDrain, kNumBars
+  kSegFull = kRowEmpty + kAhead, kTabFull = kSegFull + kSegs, kQFull = kTabFull + kTabs, kSFull0, kSFull1, kPFull, kPVDone, kEpiDone, kDrain, kNumBars
 };
-static_assert(kNumBars * 8 <= 448 && sizeof(PagedSegment) <= 64, "barriers");
+static_assert(kNumBars * 8 <= 480 && sizeof(PagedSegment) <= 64, "barriers");
 
 constexpr uint32_t kIdescQK = idesc_bf16(64, 64, 0, 0);
 constexpr uint32_t kIdescPV = idesc_bf16(128, 64, 1, 1);
@@ -150,6 +152,12 @@ __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
   return ok != 0;
 }
 
+__device__ __forceinline__ uint4 ld_shared16(uint32_t src) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(src) : "memory");
+  return v;
+}
+
 // the low half at dst, the high half kPitch behind it
 template <uint32_t kPitch>
 __device__ __forceinline__ void st_shared_halves(uint32_t dst, uint32_t v) {
@@ -183,7 +191,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
   float* alpha_s = reinterpret_cast<float*>(smem + kOffAlpha);
   float* inv_s = reinterpret_cast<float*>(smem + kOffInv);
   float* sink_s = reinterpret_cast<float*>(smem + kOffSink);
-  float* g_s = reinterpret_cast<float*>(smem + kOffG);
   float2* rope_s = reinterpret_cast<float2*>(smem + kOffRope);
 
   const int tid = threadIdx.x, lane = tid & 31;
@@ -203,6 +210,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
       mbar_init(bar(kRowEmpty + i), kGather + 64);  // the gatherers, and 64 softmax threads for all
     }
     for (int i = 0; i < kSegs; ++i) mbar_init(bar(kSegFull + i), 1);
+    for (int i = 0; i < kTabs; ++i) mbar_init(bar(kTabFull + i), 1);
     mbar_init(bar(kQFull), 256);
     mbar_init(bar(kSFull0), 1);
     mbar_init(bar(kSFull1), 1);
@@ -223,11 +231,12 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
   PagedRange* s_range = reinterpret_cast<PagedRange*>(smem + kOffMisc + 16);
   PagedSegment* segs = reinterpret_cast<PagedSegment*>(smem + kOffSeg);
   PagedSegment sg;
+  PagedRange r0 = paged_range(a, blockIdx.x, kKT, reinterpret_cast<int*>(smem + kOffKV), kSlots * kSlot / 4,
+                              reinterpret_cast<int*>(smem + kOffRed));
   if (warp == 0) {
-    PagedRange r = paged_range(a, blockIdx.x, kKT);
-    if (!paged_next(a, r, sg, kKT)) sg.n_tiles = 0;
+    if (!paged_next(a, r0, sg, kKT)) sg.n_tiles = 0;
     if (lane == 0) {
-      *s_range = r;
+      *s_range = r0;
       segs[0] = sg;
     }
   }
@@ -261,59 +270,53 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
     const int R = a.R;
     uint32_t gt = 0;
     int4 cut = make_int4(-1, 0, 0, 0);
-    uint4 va[8], vb[8];
-    float snk = 0.f;
-    auto load_q = [&]() {  // of the next segment
-      const int nh = min(kH, a.H - sg.g * kH);
-      const uint16_t* qrow = a.q + ((int64_t)sg.b * a.H + sg.g * kH) * kD + 8 * lane;
-#pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        const int h = warp + 8 * u;
-        va[u] = vb[u] = make_uint4(0, 0, 0, 0);
-        if (h < nh) {
-          va[u] = *reinterpret_cast<const uint4*>(qrow + h * kD);
-          vb[u] = *reinterpret_cast<const uint4*>(qrow + h * kD + 256);
-        }
-      }
-      if (st < nh) snk = a.sink[sg.g * kH + st];
-    };
-    reinterpret_cast<float2*>(g_s)[st] = reinterpret_cast<const float2*>(a.q_norm_g)[st];
     bool more = next_seg();
-    if (more) load_q();
     while (more) {
       const int nh = min(kH, a.H - sg.g * kH);
       const int64_t head0 = (int64_t)sg.b * a.H + sg.g * kH;
       if (sg.cut_last >= 0) cut = make_int4(sg.item, sg.cut_last, sg.slot, 0);
-      // q^ = RoPE_pos(RMSNorm(q) g), rounded to bf16 (the MMA's operand), into
+      const float2* rope_t = rope_s + (seg - 1) % kTabs * 128;
+      const float* sink_t = sink_s + (seg - 1) % kTabs * 64;
+      // q^ = RoPE_pos(RMSNorm(q) g), rounded to bf16 (the MMA's operand), in
       // the K-major operand layout: warp w takes heads w, w + 8, ..., lane l
-      // dims 8l .. 8l+7 and 256+8l ..; heads that the group does not have are
-      // 0.  Four heads' loads at a time.
-      if (st < R / 2) {
-        float cs, sn;
-        rope_cos_sin(sg.seq.pos, a.rope.t[st], &cs, &sn);
-        rope_s[st] = make_float2(cs, sn);
+      // dims 8l .. 8l+7 and 256+8l .., which are copied to where q^ will be and
+      // changed there; heads that the group does not have are 0.
+      const uint32_t qA = q_base + (uint32_t)(lane >> 3) * 8192u, qB = qA + 4u * 8192u;
+      {
+        const uint16_t* qrow = a.q + head0 * kD + 8 * lane;
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          const int h = warp + 8 * u;
+          const uint32_t sw = sw128((uint32_t)h, (uint32_t)(lane & 7)), bytes = h < nh ? 16u : 0u;
+          const uint16_t* src = h < nh ? qrow + h * kD : a.q;
+          cp_async16_or_zero(qA + sw, src, bytes);
+          cp_async16_or_zero(qB + sw, src + 256, bytes);
+        }
+        cp_async_commit();
       }
-      if (st < kH) {
-        sink_s[st] = st < nh ? snk * kLog2e : 0.f;
-        mrun[st] = kNoRef;
-      }
-      named_bar(1, 256);
+      if (st < kH) mrun[st] = kNoRef;
       {
         float2 g[8], rope[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          g[k] = *reinterpret_cast<const float2*>(g_s + 8 * lane + 2 * k);
-          g[4 + k] = *reinterpret_cast<const float2*>(g_s + 256 + 8 * lane + 2 * k);
-          const int d = 256 + 8 * lane + 2 * k - (kD - R);
-          rope[k] = d >= 0 ? rope_s[d >> 1] : make_float2(1.f, 0.f);
+          g[k] = *reinterpret_cast<const float2*>(a.q_norm_g + 8 * lane + 2 * k);
+          g[4 + k] = *reinterpret_cast<const float2*>(a.q_norm_g + 256 + 8 * lane + 2 * k);
         }
-        const uint32_t offA = (uint32_t)(lane >> 3) * 8192u, offB = (uint32_t)(4 + (lane >> 3)) * 8192u;
-#pragma unroll 1
-        for (int half = 0; half < 2; ++half) {
+        wait(kTabFull + (seg - 1) % kTabs, ((seg - 1) / kTabs) & 1u);
 #pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            const int h = warp + 8 * (4 * half + u);
-            const unsigned int wv[8] = {va[u].x, va[u].y, va[u].z, va[u].w, vb[u].x, vb[u].y, vb[u].z, vb[u].w};
+        for (int k = 0; k < 4; ++k) {
+          const int d = 256 + 8 * lane + 2 * k - (kD - R);
+          rope[k] = d >= 0 ? rope_t[d >> 1] : make_float2(1.f, 0.f);
+        }
+        cp_async_wait<0>();
+#pragma unroll 1
+        for (int u0 = 0; u0 < 8; u0 += 2) {
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const int h = warp + 8 * (u0 + u);
+            const uint32_t sw = sw128((uint32_t)h, (uint32_t)(lane & 7));
+            const uint4 va = ld_shared16(qA + sw), vb = ld_shared16(qB + sw);
+            const unsigned int wv[8] = {va.x, va.y, va.z, va.w, vb.x, vb.y, vb.z, vb.w};
             float2 acc = make_float2(0.f, 0.f);
 #pragma unroll
             for (int q = 0; q < 8; ++q) {
@@ -333,14 +336,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
               }
               pq[q] = f2_to_bf2x2(x.x, x.y);
             }
-            const uint32_t sw = sw128((uint32_t)h, (uint32_t)(lane & 7));
-            st_shared16(q_base + offA + sw, pq[0], pq[1], pq[2], pq[3]);
-            st_shared16(q_base + offB + sw, pq[4], pq[5], pq[6], pq[7]);
-          }
-#pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            va[u] = va[u + 4];
-            vb[u] = vb[u + 4];
+            st_shared16(qA + sw, pq[0], pq[1], pq[2], pq[3]);
+            st_shared16(qB + sw, pq[4], pq[5], pq[6], pq[7]);
           }
         }
       }
@@ -479,9 +476,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
       if (st < kH) {
         const float l = red[st] + red[64 + st] + red[128 + st] + red[192 + st], m = mrun[st];
         if (sg.whole) {
-          const float den = m <= kNoRef ? 0.f : l + exp2f(sink_s[st] - m);
+          const float den = m <= kNoRef ? 0.f : l + exp2f(sink_t[st] - m);
           inv_s[st] = den > 0.f ? 1.f / den : 0.f;
-          if (a.weights) a.lse2[(int64_t)sg.item * kH + st] = den > 0.f ? m + log2f(den) : sink_s[st];
+          if (a.weights) a.lse2[(int64_t)sg.item * kH + st] = den > 0.f ? m + log2f(den) : sink_t[st];
         } else {
           part[st] = m <= kNoRef ? -INFINITY : m * 0.6931471805599453f;  // natural-log units
           part[kH + st] = l;
@@ -502,8 +499,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
             // d^1 (x0 cs + x1 sn, -x0 sn + x1 cs)
             float cs = 1.f, sn = 0.f;
             if (d >= kD - R) {
-              cs = rope_s[(d - (kD - R)) >> 1].x;
-              sn = rope_s[(d - (kD - R)) >> 1].y;
+              cs = rope_t[(d - (kD - R)) >> 1].x;
+              sn = rope_t[(d - (kD - R)) >> 1].y;
               if (r & 1) sn = -sn;
             }
 #pragma unroll
@@ -545,7 +542,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
         }
       }
       more = !sg.alone && next_seg();
-      if (more) load_q();
       if (staged && st < kH) bulk_wait_read0();  // the stage is read before the next segment's q^ goes in
       named_bar(1, 256);
     }
@@ -779,8 +775,26 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
     // =================== landed rows to the MMAs ===================
     // The rows are written in the generic proxy.  The fence between the proxies
     // costs 0.2 us a chunk in the issuing warp; here it is off its path.
+    // It also makes the tables of a segment, ahead of the softmax.
     uint32_t u = 0;
     while (next_seg()) {
+      const uint32_t tab = (seg - 1) % kTabs;
+      const int nh = min(kH, a.H - sg.g * kH);
+      float2* rope_t = rope_s + tab * 128;
+      float* sink_t = sink_s + tab * 64;
+      float snk[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) snk[i] = lane + 32 * i < nh ? a.sink[sg.g * kH + lane + 32 * i] : 0.f;
+#pragma unroll 1
+      for (int i = lane; i < a.R / 2; i += 32) {
+        float cs, sn;
+        rope_cos_sin(sg.seq.pos, a.rope.t[i], &cs, &sn);
+        rope_t[i] = make_float2(cs, sn);
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) sink_t[lane + 32 * i] = snk[i] * kLog2e;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kTabFull + tab));
       for (int i = 4 * sg.n_tiles; i > 0; --i, ++u) {
         wait(kKVLanded + u % kSlots, (u / kSlots) & 1u);
         fence_async_smem();
