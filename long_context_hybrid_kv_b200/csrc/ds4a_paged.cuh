@@ -124,7 +124,7 @@ __device__ __forceinline__ int paged_item_seq(const PagedArgs& a, int item) {
 
 // Items of at most this many tiles are not cut, and no piece is shorter.
 constexpr int kPagedWhole = 4, kPagedLeast = 2;
-constexpr int kPagedCost = 6;  // of a segment besides its tiles, in tiles (measured: 14 us a second segment)
+constexpr int kPagedCost = 6;  // of a segment besides its tiles, in tiles (a second segment takes 7 to 8 us, four tiles; 4 to 6 measure alike)
 constexpr int kPagedJoin = 4;  // of the joining, in tiles
 
 // More items than blocks: the blocks that take part, where block c's range
