@@ -15,7 +15,8 @@
  * - Ownership: the caller owns every buffer.  The library allocates nothing
  *   per call; scratch memory ("workspace") is passed in by the caller and
  *   sized by the *_workspace queries.  Library state: one device error word
- *   per device, and an optional launch trace (ds4a_trace_*), off by default.
+ *   per device, an optional launch trace (ds4a_trace_*), off by default, and
+ *   a host thread's last table of RoPE frequencies.
  * - Execution: every call is asynchronous on the given CUDA stream (NULL =
  *   the legacy default stream).  Pointers named "device" must be device (or
  *   managed) memory of the current device; "host" pointers are host memory.
@@ -495,7 +496,9 @@ size_t ds4a_paged_attend_workspace(const ds4a_layer_cfg* cfg, const ds4a_paged_k
  *   ws      device workspace of ds4a_paged_attend_workspace(...) bytes; two
  *           calls that may run at the same time need one each
  * The launch does not depend on the positions, so that a captured graph
- * serves later steps as the sequences grow.
+ * serves later steps as the sequences grow.  A call whose tables reach more
+ * than 2^27 tiles in all (64 keys of a group of 64 heads for rows of 512, else
+ * 32 keys of a group of 8) is refused (DS4A_EINVAL).
  */
 int ds4a_paged_attend(const ds4a_layer_cfg* cfg, const ds4a_paged_kv* kv, int B, const int32_t* q_pos,
                       const ds4a_bf16* q, const float* q_norm_g, const int32_t* drop, const int32_t* idx,

@@ -566,7 +566,7 @@ static size_t paged_layout(const ds4a_layer_cfg* cfg, const ds4a_paged_kv* kv, i
   a->hgroups = (a->H + a->hn - 1) / a->hn;
   const int64_t keys = (int64_t)(sparse ? min(a->k, a->cap) : a->cap) + a->W;
   const int64_t items = (int64_t)B * a->hgroups, tiles = items * ((keys + a->kt - 1) / a->kt);
-  if (tiles > INT32_MAX) return 0;
+  if (tiles > 1 << 27) return 0;  // the schedule counts in ints, a segment's cost and its double among them
   a->G = (int)(tiles < a->G ? (tiles > 0 ? tiles : 1) : a->G);
   size_t at = 0;
   auto take = [&](size_t bytes) {
@@ -623,7 +623,15 @@ int ds4a_paged_attend(const ds4a_layer_cfg* cfg, const ds4a_paged_kv* kv, int B,
   a.drop = drop; a.q_pos = q_pos; a.q = q; a.q_norm_g = q_norm_g; a.idx = idx;
   a.win = win; a.win_cap = win_cap; a.win_bstride = win_bstride; a.sink = sink; a.out = out;
   a.weights = weights; a.w_stride = w_stride; a.w_len = w_len;
-  fill_rope_theta(&a.rope, a.R, cfg->rope_base);
+  // (32 pow() are most of a small call's time on the host: kept for the layers that follow)
+  struct Theta { int R = -1; float base = 0.f; RopeTheta t; };
+  static thread_local Theta theta;
+  if (theta.R != a.R || theta.base != cfg->rope_base) {
+    fill_rope_theta(&theta.t, a.R, cfg->rope_base);
+    theta.R = a.R;
+    theta.base = cfg->rope_base;
+  }
+  a.rope = theta.t;
   a.err = err_word();
   if (!a.err) return DS4A_ECUDA;
   cudaStream_t s = (cudaStream_t)stream;

@@ -63,6 +63,8 @@ class PagedKv(ctypes.Structure):
     _fields_ = [("pages", ctypes.c_void_p), ("table", ctypes.c_void_p), ("table_stride", ctypes.c_int64),
                 ("format", ctypes.c_int32), ("n_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
                 ("max_pages", ctypes.c_int32)]
+    # what paged_kv knows besides: the tensors, their device, the table's rows, elements of a page's row
+    held = dev = rows = row_size = None
 
 
 def layer_cfg(c) -> LayerCfg:
@@ -364,20 +366,51 @@ def ds4a_out_proj(cfg: OprojCfg, o, w_a, w_b, mid, y, ws=None, *, stream=None):
     _ok(rc, "ds4a_out_proj")
 
 
-def _rows(t, dtype, name, B=None):
+_gpus = None
+
+
+def _here() -> int:
+    """The current device, where the paged and MXFP4 calls run and their
+    tensors must be (-1 without one)."""
+    import torch
+    global _gpus
+    if _gpus is None:
+        _gpus = torch.cuda.is_available()
+    return torch.cuda.current_device() if _gpus else -1
+
+
+def _rows(t, dtype, name, B=None, dev=None):
     """A matrix of one row per sequence whose rows are contiguous: (width, stride)."""
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1) or (B is not None and t.shape[0] != B):
         raise ValueError(f"{name} must be [{'B' if B is None else B}, n] with contiguous rows")
+    if dev is not None and t.get_device() != dev:
+        raise ValueError(f"{name} must be on the current device")
     return t.shape[1], (t.stride(0) if t.shape[0] > 1 else max(1, t.shape[1]))
 
 
-def _vec(t, B, name):
-    import torch
-    if t is not None and (t.dtype != torch.int32 or t.shape != (B,) or not t.is_contiguous()):
-        raise ValueError(f"{name} must be contiguous int32 [{B}]")
-    return t
+def _flat(t, dtype, n, name, dev, least=False):
+    """Address of a contiguous tensor of n elements (least: or more) on the current device."""
+    if t.get_device() != dev or not t.is_contiguous() or (t.numel() < n if least else t.numel() != n) or \
+            t.dtype != dtype:
+        raise ValueError(f"{name} must be contiguous {dtype} of {n} elements on the current device")
+    return t.data_ptr()
+
+
+def _work(ws, dev):
+    if ws is None:
+        return None, 0
+    if ws.get_device() != dev or not ws.is_contiguous():
+        raise ValueError("ws must be contiguous and on the current device")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
+
+
+def _kv_of(kv, B, dev):
+    if kv.dev is not None and kv.dev != dev:
+        raise ValueError("pages and table must be on the current device")
+    if kv.rows is not None and kv.rows < B:
+        raise ValueError(f"the page table must have {B} rows")
 
 
 def paged_kv(pages, table, page_size: int, *, fmt: int = 0) -> PagedKv:
@@ -392,9 +425,19 @@ def paged_kv(pages, table, page_size: int, *, fmt: int = 0) -> PagedKv:
     if pages.dim() != 3 or pages.shape[1] != page_size:
         raise ValueError("pages must be [n_pages, page_size, row]")
     width, stride = _rows(table, torch.int32, "table")
+    if table.get_device() != pages.get_device():
+        raise ValueError("pages and table must be on one device")
     kv = PagedKv(pages.data_ptr(), table.data_ptr(), stride, fmt, pages.shape[0], page_size, width)
-    kv.held = (pages, table)
+    kv.held, kv.dev, kv.rows, kv.row_size = (pages, table), pages.get_device(), table.shape[0], pages.shape[2]
     return kv
+
+
+def _row_of(cfg, kv):
+    if kv.row_size is None:
+        return
+    want = cfg.head_dim if kv.format == 0 else ds4a_kv_fp8_row_bytes(cfg.head_dim, cfg.rope_dim)
+    if kv.row_size != want:
+        raise ValueError(f"the pages' rows must have {want} elements")
 
 
 def ds4a_paged_attend_workspace(cfg: LayerCfg, kv: PagedKv, B: int, sparse: bool = False, weights: bool = False) -> int:
@@ -406,29 +449,54 @@ def ds4a_paged_attend(cfg: LayerCfg, kv: PagedKv, q_pos, q, q_norm_g, win, win_c
                       idx=None, weights=None, stream=None):
     """One new token per sequence: q, out [B, H, D], q_pos [B]; idx int32
     [B, k] selects slots; weights bf16 [B, n] receives each slot's attention."""
-    _bf16(q, "q"), _bf16(out, "out"), _bf16(win, "win")
-    B = q.shape[0]
-    _vec(q_pos, B, "q_pos"), _vec(drop, B, "drop")
+    import torch
+    bf, f32, i32, dev = torch.bfloat16, torch.float32, torch.int32, _here()
+    B, H, D = q.shape[0], cfg.n_heads, cfg.head_dim
+    _kv_of(kv, B, dev), _row_of(cfg, kv)
     w_len = w_stride = 0
     if weights is not None:
-        w_len, w_stride = _rows(weights, q.dtype, "weights", B)
-    rc = lib().ds4a_paged_attend(cfg, kv, B, q_pos.data_ptr(), q.data_ptr(), q_norm_g.data_ptr(), _ptr(drop),
-                                 _ptr(idx), _ptr(win), win_cap, 0 if win is None else win.stride(0), sink.data_ptr(),
-                                 out.data_ptr(), _ptr(weights), w_len, w_stride, _ptr(ws),
-                                 0 if ws is None else ws.numel() * ws.element_size(), _stream(stream))
+        w_len, w_stride = _rows(weights, bf, "weights", B, dev)
+    if win is not None and (win.dtype != bf or win.get_device() != dev or win.dim() != 3 or win.shape[0] != B or
+                            win.shape[1] < win_cap or win.shape[2] != D or win.stride(2) != 1 or win.stride(1) != D):
+        raise ValueError("win must be bfloat16 [B, win_cap, head_dim] on the current device, its rows contiguous")
+    n = B * H * D
+    if not (q.get_device() == q_pos.get_device() == out.get_device() == sink.get_device() == q_norm_g.get_device() == dev
+            and q.numel() == out.numel() == n and q_pos.numel() == B and sink.numel() == H and q_norm_g.numel() == D
+            and q.dtype == out.dtype == bf and q_pos.dtype == i32 and sink.dtype == q_norm_g.dtype == f32
+            and q.is_contiguous() and out.is_contiguous() and q_pos.is_contiguous() and sink.is_contiguous()
+            and q_norm_g.is_contiguous()):  # (which one)
+        _flat(q_pos, i32, B, "q_pos", dev), _flat(q, bf, n, "q", dev), _flat(q_norm_g, f32, D, "q_norm_g", dev)
+        _flat(sink, f32, H, "sink", dev), _flat(out, bf, n, "out", dev)
+    p_ws, n_ws = _work(ws, dev)
+    rc = lib().ds4a_paged_attend(cfg, kv, B, q_pos.data_ptr(), q.data_ptr(), q_norm_g.data_ptr(),
+                                 None if drop is None else _flat(drop, i32, B, "drop", dev),
+                                 None if idx is None else _flat(idx, i32, B * cfg.topk, "idx", dev), _ptr(win), win_cap,
+                                 0 if win is None else win.stride(0), sink.data_ptr(), out.data_ptr(), _ptr(weights),
+                                 w_len, w_stride, p_ws, n_ws, _stream(stream))
     _ok(rc, "ds4a_paged_attend")
 
 
 def ds4a_paged_append(cfg: LayerCfg, kv: PagedKv, pos, ca, za, bias_a, state, *, drop=None, cb=None, zb=None,
                       bias_b=None, norm_g=None, stream=None):
     """ds4a_compress_append of new rows [B, D] into a paged cache (slot = entry - drop)."""
-    _bf16(ca, "ca"), _bf16(za, "za"), _bf16(cb, "cb"), _bf16(zb, "zb")
-    B = ca.shape[0]
-    _vec(pos, B, "pos"), _vec(drop, B, "drop")
-    if ca.shape[1] != cfg.head_dim:
+    import torch
+    bf, f32, i32, dev = torch.bfloat16, torch.float32, torch.int32, _here()
+    B, c = ca.shape
+    if c != cfg.head_dim:
         raise ValueError("a paged cache holds K=V entries of head_dim channels")
-    rc = lib().ds4a_paged_append(cfg, kv, B, _ptr(pos), _ptr(drop), _ptr(ca), _ptr(cb), _ptr(za), _ptr(zb),
-                                 _ptr(bias_a), _ptr(bias_b), _ptr(norm_g), _ptr(state), _stream(stream))
+    _kv_of(kv, B, dev)
+    if norm_g is not None:  # (RoPE, and FP8 rows, come with the norm)
+        _row_of(cfg, kv)
+    some = lambda t, dtype, n, name: None if t is None else _flat(t, dtype, n, name, dev)  # noqa: E731
+    need = ds4a_compress_state_bytes(cfg, B, c, cb is not None)
+    if state.get_device() != dev or not state.is_contiguous() or state.numel() * state.element_size() < need:
+        raise ValueError(f"state must be contiguous, of {need} bytes and on the current device")
+    rc = lib().ds4a_paged_append(cfg, kv, B, _flat(pos, i32, B, "pos", dev), some(drop, i32, B, "drop"),
+                                 _flat(ca, bf, B * c, "ca", dev), some(cb, bf, B * c, "cb"),
+                                 _flat(za, bf, B * c, "za", dev), some(zb, bf, B * c, "zb"),
+                                 _flat(bias_a, f32, cfg.ratio * c, "bias_a", dev),
+                                 some(bias_b, f32, cfg.ratio * c, "bias_b"), some(norm_g, f32, c, "norm_g"),
+                                 state.data_ptr(), _stream(stream))
     _ok(rc, "ds4a_paged_append")
 
 
@@ -441,19 +509,20 @@ def ds4a_paged_evict(cfg: LayerCfg, kv: PagedKv, q_pos, budget: int, recent: int
     """acc (float32) += weights (bf16), entry (int32), all [B, n_slots]; caches
     of more than budget entries are cut to it in place, drop [B] follows."""
     import torch
-    B = q_pos.shape[0]
-    _vec(q_pos, B, "q_pos"), _vec(drop, B, "drop")
-    n, stride = _rows(acc, torch.float32, "acc", B)
-    if _rows(entry, torch.int32, "entry", B) != (n, stride):
+    i32, dev, B = torch.int32, _here(), q_pos.shape[0]
+    _kv_of(kv, B, dev), _row_of(cfg, kv)
+    n, stride = _rows(acc, torch.float32, "acc", B, dev)
+    if _rows(entry, i32, "entry", B, dev) != (n, stride):
         raise ValueError("acc and entry must have the same shape and stride")
     w_stride = 0
     if weights is not None:
-        w_len, w_stride = _rows(weights, torch.bfloat16, "weights", B)
+        w_len, w_stride = _rows(weights, torch.bfloat16, "weights", B, dev)
         if w_len < n:
             raise ValueError("weights must cover the slots of acc")
-    rc = lib().ds4a_paged_evict(cfg, kv, B, q_pos.data_ptr(), _ptr(weights), w_stride, budget, recent, n,
-                                acc.data_ptr(), entry.data_ptr(), stride, drop.data_ptr(), _ptr(ws),
-                                0 if ws is None else ws.numel() * ws.element_size(), _stream(stream))
+    p_ws, n_ws = _work(ws, dev)
+    rc = lib().ds4a_paged_evict(cfg, kv, B, _flat(q_pos, i32, B, "q_pos", dev), _ptr(weights), w_stride, budget, recent,
+                                n, acc.data_ptr(), entry.data_ptr(), stride, _flat(drop, i32, B, "drop", dev), p_ws,
+                                n_ws, _stream(stream))
     _ok(rc, "ds4a_paged_evict")
 
 
@@ -461,22 +530,15 @@ def ds4a_mxfp4_scale_bytes(rows: int, K: int) -> int:
     return lib().ds4a_mxfp4_scale_bytes(rows, K)
 
 
-def _u8(t, n, name):
-    import torch
-    if t.dtype != torch.uint8 or not t.is_contiguous() or t.numel() < n:
-        raise ValueError(f"{name} must be contiguous uint8 of at least {n} bytes")
-    return t.data_ptr()
-
-
 def ds4a_quantize_mxfp4(rows, codes, scales, *, stream=None):
     """bf16 rows [n, K] (rows may lie apart) -> E2M1 codes [n, K/2] and E8M0
     scales in the products' order (ds4a_mxfp4_scale_bytes(n, K) bytes)."""
     import torch
-    n, K = rows.shape
-    if rows.dtype != torch.bfloat16 or (K > 1 and rows.stride(1) != 1):
-        raise ValueError("rows must be bfloat16 [n, K] with contiguous rows")
-    rc = lib().ds4a_quantize_mxfp4(n, K, _ptr(rows), rows.stride(0) if n > 1 else K, _u8(codes, n * K // 2, "codes"),
-                                   _u8(scales, ds4a_mxfp4_scale_bytes(n, K), "scales"), _stream(stream))
+    u8, dev, n = torch.uint8, _here(), rows.shape[0]
+    K, stride = _rows(rows, torch.bfloat16, "rows", n, dev)
+    rc = lib().ds4a_quantize_mxfp4(n, K, rows.data_ptr(), stride, _flat(codes, u8, n * K // 2, "codes", dev, True),
+                                   _flat(scales, u8, ds4a_mxfp4_scale_bytes(n, K), "scales", dev, True),
+                                   _stream(stream))
     _ok(rc, "ds4a_quantize_mxfp4")
 
 
@@ -486,13 +548,16 @@ def ds4a_out_proj_mxfp4_workspace(cfg: OprojCfg, M: int) -> int:
 
 def ds4a_out_proj_mxfp4(cfg: OprojCfg, o, wa_codes, wa_scales, wb_codes, wb_scales, y, ws, *, stream=None):
     """o [M, H, D] -> y [M, hidden], weights and activations in MXFP4."""
-    _bf16(o, "o"), _bf16(y, "y")
+    import torch
+    bf, u8, dev, M = torch.bfloat16, torch.uint8, _here(), o.shape[0]
     n1, k1 = cfg.n_groups * cfg.group_rank, cfg.n_heads // max(1, cfg.n_groups) * cfg.head_dim
-    rc = lib().ds4a_out_proj_mxfp4(cfg, o.shape[0], o.data_ptr(), _u8(wa_codes, n1 * k1 // 2, "wa_codes"),
-                                   _u8(wa_scales, n1 * k1 // 32, "wa_scales"),
-                                   _u8(wb_codes, cfg.hidden * n1 // 2, "wb_codes"),
-                                   _u8(wb_scales, cfg.hidden * n1 // 32, "wb_scales"), y.data_ptr(), _ptr(ws),
-                                   0 if ws is None else ws.numel() * ws.element_size(), _stream(stream))
+    p_ws, n_ws = _work(ws, dev)
+    rc = lib().ds4a_out_proj_mxfp4(cfg, M, _flat(o, bf, M * cfg.n_heads * cfg.head_dim, "o", dev),
+                                   _flat(wa_codes, u8, n1 * k1 // 2, "wa_codes", dev, True),
+                                   _flat(wa_scales, u8, n1 * k1 // 32, "wa_scales", dev, True),
+                                   _flat(wb_codes, u8, cfg.hidden * n1 // 2, "wb_codes", dev, True),
+                                   _flat(wb_scales, u8, cfg.hidden * n1 // 32, "wb_scales", dev, True),
+                                   _flat(y, bf, M * cfg.hidden, "y", dev), p_ws, n_ws, _stream(stream))
     _ok(rc, "ds4a_out_proj_mxfp4")
 
 

@@ -85,6 +85,10 @@ def test_attend_other_refusals():
     # an FP8 row holds whole 32-value blocks
     assert attend(c=cfg(head_dim=488), k=kv(format=L.DS4A_MX_KV_FP8)) == L.DS4A_EUNSUPPORTED
     assert L.ds4a_paged_attend_workspace(cfg(), kv(), 0) == 0
+    # more tiles than the schedule counts
+    far = kv(max_pages=1 << 24, table_stride=1 << 24)
+    assert L.ds4a_paged_attend_workspace(cfg(), far, 4) > 0 and L.ds4a_paged_attend_workspace(cfg(), far, 65535) == 0
+    assert attend(k=far, B=65535) == L.DS4A_EINVAL
     assert L.ds4a_paged_attend_workspace(cfg(), kv(), 2, weights=True) > need
 
 

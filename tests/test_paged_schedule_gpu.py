@@ -1,0 +1,141 @@
+"""Every way in which decode attention over the paged cache spreads a batch
+over the GPU, against the plain 64-bit form: pieces of cut items, short items
+that share blocks, the row of all tiles cut into ranges; with head groups,
+FP8 rows, items of many pieces, and the refusals of the binding that need a
+device."""
+import numpy as np
+import pytest
+import torch
+
+import long_context_hybrid_kv_b200 as L
+from gpu_util import check_ok, i32
+from test_paged_gpu import Case, _evict_case
+
+pytestmark = pytest.mark.gpu
+
+
+def spread(name, lens, weights=True, **kw):
+    c = Case(name, lens, kw.pop("page", 64), m=16, **kw)
+    w = torch.full((c.B, max(lens) + 1), 7.0, dtype=torch.bfloat16, device="cuda") if weights else None
+    c.run(weights=w)
+    check_ok()
+    c.check(weights=w)
+    first = c.out.clone()
+    c.out.fill_(7.0)
+    c.run(weights=w)  # the same bits from a workspace of other leftovers
+    check_ok()
+    assert torch.equal(first, c.out)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("H", [8, 72])
+def test_pieces_next_to_shared_blocks(H, fp8):
+    # long items cut into pieces, short ones that share blocks, none at all
+    spread(f"pieces{H}{fp8}", [9000, 3, 0, 700, 64, 1, 130, 65, 2500, 40, 256, 129], H=H, fp8=fp8)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_equal_items_as_a_row_of_tiles(fp8):
+    # 100 items of 24 tiles: one a block would leave a third of the blocks idle
+    spread(f"row{fp8}", [1400] * 100, H=8, fp8=fp8, weights=not fp8)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_more_items_than_blocks_as_a_row_of_tiles(fp8):
+    # 152 items of 20 tiles on 148 blocks; some short ones whose ends move
+    spread(f"many{fp8}", [1150] * 100 + [70, 1, 0, 200] * 10 + [1150] * 52, H=5, fp8=fp8, weights=not fp8)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_more_items_than_blocks_share_them(fp8):
+    lens = [int(v) for v in np.random.default_rng(3).integers(0, 300, 290)]
+    spread(f"share{fp8}", lens, H=6, fp8=fp8, page=16)
+
+
+def test_more_items_than_blocks_by_head_groups():
+    # 80 sequences x 2 groups of heads
+    lens = [int(v) for v in np.random.default_rng(4).integers(0, 500, 80)]
+    spread("groups", lens, H=70, page=16)
+
+
+def test_many_pieces_of_two_head_groups():
+    # each group's item is cut into more pieces than one warp joins at once
+    spread("long groups", [4000], H=100)
+
+
+def test_without_a_window_empty_sequences_between_cut_ones():
+    spread("nowin", [0, 3000, 0, 0, 1, 2000, 0], H=8, W=0)
+
+
+def test_selected_slots_of_many_sequences():
+    lens = [int(v) for v in np.random.default_rng(5).integers(0, 700, 170)]
+    c = Case("selmany", lens, 16, m=16, H=4)
+    k = 300
+    cfg = L.LayerCfg(4, 512, 64, 128, 64, 128, k, 16, 512 ** -0.5, 10000.0, 1e-6)
+    c.cfg = cfg
+    idx = np.full((c.B, k), -1, np.int32)
+    slots = []
+    rng = np.random.default_rng(6)
+    for b, n in enumerate(lens):
+        take = np.sort(rng.choice(n, min(n, k), replace=False)) if n else np.zeros(0, np.int64)
+        idx[b, :len(take)] = take
+        slots.append(take)
+    c.run(idx=i32(idx))
+    check_ok()
+    c.check(slots=slots)
+
+
+def test_generic_shape_of_many_sequences():
+    lens = [int(v) for v in np.random.default_rng(7).integers(0, 120, 320)]
+    spread("generic", lens, H=3, D=64, R=16, W=8, page=7)
+
+
+@pytest.mark.parametrize("cap", [1024, 1025, 4096, 8192, 8193, 16384, 32768, 32769])
+def test_evict_every_size_of_cache(cap):
+    # a block's threads hold 1, 4, 8, 16 or 32 slots each; above that two launches
+    _evict_case(f"size{cap}", [cap, cap - 1, cap // 2 + 1], cap, cap // 2, 7, 32)
+
+
+def test_binding_refuses_other_devices_and_sizes():
+    c = Case("refuse", [40, 100], 16, m=16, H=8)
+    ws = c.workspace()
+
+    def call(**kw):
+        a = dict(kv=c.kv, q_pos=c.d_pos, q=c.d_q, g=c.d_g, win=c.d_win, sink=c.d_sink, out=c.out, ws=ws)
+        a.update(kw)
+        L.ds4a_paged_attend(c.cfg, a["kv"], a["q_pos"], a["q"], a["g"], a["win"], c.win_cap, a["sink"], a["out"], a["ws"],
+                            drop=a.get("drop"), idx=a.get("idx"), weights=a.get("weights"))
+
+    call()
+    for bad in (dict(q_pos=c.d_pos.cpu()), dict(q=c.d_q.cpu()), dict(g=c.d_g.cpu()), dict(win=c.d_win.cpu()),
+                dict(sink=c.d_sink.cpu()), dict(out=c.out.cpu()), dict(ws=ws.cpu()), dict(drop=c.d_pos.cpu()),
+                dict(kv=L.paged_kv(c.pages.cpu(), c.d_table.cpu(), 16)), dict(kv=L.paged_kv(c.pages, c.d_table[:1], 16)),
+                dict(kv=L.paged_kv(c.pages[..., :256].contiguous(), c.d_table, 16)),
+                dict(q=c.d_q[:, :7].contiguous()), dict(out=c.out[:, :7].contiguous()), dict(g=c.d_g[:511]),
+                dict(sink=c.d_sink[:7]), dict(win=c.d_win[:, :100]), dict(win=c.d_win[:1]),
+                dict(q_pos=c.d_pos.long()), dict(idx=c.d_table[:, :2].contiguous()),
+                dict(weights=torch.zeros((1, 200), dtype=torch.bfloat16, device="cuda")),
+                dict(weights=torch.zeros((2, 200), dtype=torch.bfloat16))):
+        with pytest.raises(ValueError):
+            call(**bad)
+    with pytest.raises(ValueError):
+        L.paged_kv(c.pages, c.d_table.cpu(), 16)
+    B, n = 2, 128
+    acc, entry = torch.zeros((B, n), device="cuda"), torch.full((B, n), -1, dtype=torch.int32, device="cuda")
+    drop = torch.zeros(B, dtype=torch.int32, device="cuda")
+    ews = torch.zeros(L.ds4a_paged_evict_workspace(c.kv, B), dtype=torch.uint8, device="cuda")
+    for bad in (dict(acc=acc.cpu()), dict(entry=entry.cpu()), dict(drop=drop.cpu()), dict(q_pos=c.d_pos.cpu()),
+                dict(ws=ews.cpu()), dict(drop=drop[:1])):
+        a = dict(q_pos=c.d_pos, acc=acc, entry=entry, drop=drop, ws=ews)
+        a.update(bad)
+        with pytest.raises(ValueError):
+            L.ds4a_paged_evict(c.cfg, c.kv, a["q_pos"], 64, 8, a["acc"], a["entry"], a["drop"], a["ws"])
+    o = torch.zeros((2, 8, 512), dtype=torch.bfloat16, device="cuda")
+    oc = L.OprojCfg(8, 512, 8, 128, 256)
+    u = lambda k: torch.zeros(k, dtype=torch.uint8, device="cuda")  # noqa: E731
+    args = [o, u(8 * 128 * 512 // 2), u(8 * 128 * 512 // 32), u(256 * 1024 // 2), u(256 * 1024 // 32),
+            torch.zeros((2, 256), dtype=torch.bfloat16, device="cuda"), u(L.ds4a_out_proj_mxfp4_workspace(oc, 2))]
+    for i in range(7):
+        with pytest.raises(ValueError):
+            L.ds4a_out_proj_mxfp4(oc, *[t.cpu() if j == i else t for j, t in enumerate(args)])
+    check_ok()
