@@ -422,10 +422,13 @@ __global__ void __launch_bounds__(128) mxfp4_finish_kernel(const GemmParams p) {
 // better, and a block's ring holds half of its loads or all of them, the
 // weights' out before the kernel ahead has ended.  The first product quantises
 // its rows of o straight into the operand (a 32-value block is one 16-byte
-// piece of the swizzled row), four warps a stage, so no kernel does it
-// before.  The blocks of a cluster leave their float sums in shared memory and
+// piece of the swizzled row), four warps a stage and two blocks a thread at a
+// time (four took 2 us longer for 77 rows: at a first pass instructions cost
+// more than waiting), so no kernel does it before.  The blocks of a cluster leave their float sums in shared memory and
 // each adds a share of the columns, in the order of the splits, and finishes
-// it: two launches in all instead of five.
+// it: two launches in all instead of five.  64 heads x 512 -> 8 x 1024 -> 4096,
+// both products: 16.0 us for one row, 17.5 for 16, 23.4 for 77, 27.7 for 128;
+// the weights alone take 5.5 us.
 // ---------------------------------------------------------------------------
 constexpr int kQuantWarps = 16;  // that quantise; the first four of them read the sums
 constexpr int kSmallThreads = 64 + 32 * kQuantWarps;
@@ -555,16 +558,16 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
         if (j >= S::kRing) mbar_wait(empty(j), (j / S::kRing - 1) & 1u, abort_flag, err);
         unsigned char* st = smem + (j % S::kRing) * S::kStage;
         const uint16_t* src = o + ((int64_t)a_blk + 2 * (k0 + j)) * 128;
-        for (int i0 = t; i0 < p.M * 8; i0 += 4 * kT) {
-          uint4 u[4][4];
+        for (int i0 = t; i0 < p.M * 8; i0 += 2 * kT) {
+          uint4 u[2][4];
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
+          for (int q = 0; q < 2; ++q) {
             const int i = min(i0 + kT * q, p.M * 8 - 1);
 #pragma unroll
             for (int c = 0; c < 4; ++c) u[q][c] = reinterpret_cast<const uint4*>(src + (i >> 3) * o_cols + (i & 7) * 32)[c];
           }
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
+          for (int q = 0; q < 2; ++q) {
             const int i = i0 + kT * q, row = i >> 3, blk = i & 7;
             if (i >= p.M * 8) break;
             uint4 codes;
@@ -609,12 +612,13 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
   pdl_wait();
   if (p.ksplit > 1) cluster_sync();
   // this block's columns of the tile: eight threads a 32-column block
-  const int cols = kN / p.ksplit, c_base = split * cols, per = cols / 4;  // threads a row
+  const int cols = kN / p.ksplit, c_base = split * cols, per = cols / 4, sh = __ffs(per) - 1;  // threads a row (ksplit 1, 2 or 4)
   const int used = (p.k_steps + p.steps_per_split - 1) / p.steps_per_split;  // splits with steps
   // (of the operand's padding rows neither codes nor scales are written: they
   // only reach padding rows of the next sums)
+#pragma unroll 1
   for (int i = tid; i < p.M * per; i += kSmallThreads) {
-    const int row = i / per, c = c_base + (i - row * per) * 4, col = n0 + c;
+    const int row = i >> sh, c = c_base + (i & (per - 1)) * 4, col = n0 + c;
     const uint32_t at = (uint32_t)row * S::kPitch + (uint32_t)c * 4u;
     float4 y[4];
 #pragma unroll
