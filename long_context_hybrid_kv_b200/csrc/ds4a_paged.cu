@@ -259,30 +259,41 @@ __device__ __forceinline__ void join_sum(const PagedArgs& a, int c0, int slot0, 
 __device__ __forceinline__ void join_out(const PagedArgs& a, int item, int hl, int d0, const JoinSum& j, int pos, float sk) {
   const int lane = threadIdx.x & 31, D = a.D;
   const int b = paged_item_seq(a, item), h = (item - b * a.hgroups) * a.hn + hl;
+  float x[8];
   const float inv = j.M == -INFINITY ? 0.f : 1.f / (j.L + __expf(sk - j.M));
   if (a.weights && lane == 0 && d0 == 0) {
     const float top = fmaxf(j.M, sk);
     a.lse2[(int64_t)item * a.hn + hl] = (top + logf(j.L * expf(j.M - top) + expf(sk - top))) * kLog2e;
   }
 #pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] = j.x[i] * inv;
+  // rotation by -pos: a lane finds the angle of one pair in 32 and has the
+  // others' from its neighbours (one place that computes angles, not four: a
+  // short kernel waits for its instructions)
+  const int r0 = D - a.R;
+  if (d0 + 256 > r0) {
+#pragma unroll 1
+    for (int p0 = 0; 2 * p0 < a.R; p0 += 32) {
+      float cs, sn;
+      rope_cos_sin(pos, a.rope.t[min(p0 + lane, kMaxRopePairs - 1)], &cs, &sn);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int dd = d0 + 4 * lane + 128 * (i >> 1) + 2 * (i & 1) - r0, pr = dd >> 1;
+        const float c1 = __shfl_sync(0xffffffffu, cs, pr & 31), s1 = __shfl_sync(0xffffffffu, sn, pr & 31);
+        if (dd >= 0 && (pr & ~31) == p0) {
+          const float x0 = x[2 * i], x1 = x[2 * i + 1];
+          x[2 * i] = x0 * c1 + x1 * s1;
+          x[2 * i + 1] = -x0 * s1 + x1 * c1;
+        }
+      }
+    }
+  }
+#pragma unroll
   for (int k = 0; k < 2; ++k) {
     const int d = d0 + 4 * lane + 128 * k;
-    if (d >= D) continue;
-    unsigned int w[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      float x0 = j.x[4 * k + 2 * i] * inv, x1 = j.x[4 * k + 2 * i + 1] * inv;
-      const int dd = d + 2 * i;
-      if (dd >= D - a.R) {
-        float cs, sn;
-        rope_cos_sin(pos, a.rope.t[(dd - (D - a.R)) >> 1], &cs, &sn);
-        const float y0 = x0 * cs + x1 * sn;
-        x1 = -x0 * sn + x1 * cs;
-        x0 = y0;
-      }
-      w[i] = f2_to_bf2x2(x0, x1);
-    }
-    *reinterpret_cast<uint2*>(a.out + ((int64_t)b * a.H + h) * D + d) = make_uint2(w[0], w[1]);
+    if (d < D)
+      *reinterpret_cast<uint2*>(a.out + ((int64_t)b * a.H + h) * D + d) =
+          make_uint2(f2_to_bf2x2(x[4 * k], x[4 * k + 1]), f2_to_bf2x2(x[4 * k + 2], x[4 * k + 3]));
   }
 }
 
