@@ -511,18 +511,25 @@ def ds4a_paged_evict(cfg: LayerCfg, kv: PagedKv, q_pos, budget: int, recent: int
     import torch
     i32, dev, B = torch.int32, _here(), q_pos.shape[0]
     _kv_of(kv, B, dev), _row_of(cfg, kv)
-    n, stride = _rows(acc, torch.float32, "acc", B, dev)
-    if _rows(entry, i32, "entry", B, dev) != (n, stride):
-        raise ValueError("acc and entry must have the same shape and stride")
+    if not (q_pos.get_device() == drop.get_device() == acc.get_device() == entry.get_device() == dev
+            and q_pos.dtype == drop.dtype == entry.dtype == i32 and acc.dtype == torch.float32
+            and q_pos.numel() == drop.numel() == B and acc.dim() == 2 and acc.shape == entry.shape and acc.shape[0] == B
+            and q_pos.is_contiguous() and drop.is_contiguous() and acc.is_contiguous() and entry.is_contiguous()):
+        _flat(q_pos, i32, B, "q_pos", dev), _flat(drop, i32, B, "drop", dev)
+        n, stride = _rows(acc, torch.float32, "acc", B, dev)  # (rows may lie apart)
+        if _rows(entry, i32, "entry", B, dev) != (n, stride):
+            raise ValueError("acc and entry must have the same shape and stride")
+    else:
+        n = stride = acc.shape[1]
     w_stride = 0
     if weights is not None:
         w_len, w_stride = _rows(weights, torch.bfloat16, "weights", B, dev)
         if w_len < n:
             raise ValueError("weights must cover the slots of acc")
     p_ws, n_ws = _work(ws, dev)
-    rc = lib().ds4a_paged_evict(cfg, kv, B, _flat(q_pos, i32, B, "q_pos", dev), _ptr(weights), w_stride, budget, recent,
-                                n, acc.data_ptr(), entry.data_ptr(), stride, _flat(drop, i32, B, "drop", dev), p_ws,
-                                n_ws, _stream(stream))
+    rc = lib().ds4a_paged_evict(cfg, kv, B, q_pos.data_ptr(), _ptr(weights), w_stride, budget, recent, n,
+                                acc.data_ptr(), entry.data_ptr(), stride, drop.data_ptr(), p_ws, n_ws,
+                                _stream(stream))
     _ok(rc, "ds4a_paged_evict")
 
 
