@@ -185,8 +185,10 @@ __global__ void __launch_bounds__(kGenThreads) paged_attend_generic_kernel(const
 // item, of up to eight segments, takes two warps a head: the lanes hold the
 // segments' maxima, and a lane sums 8 dims of half a head.  An item of more
 // segments (few long sequences) takes a block for each half head, its warps an
-// eighth of the segments each, added in order.  Bound by latency: three dependent reads from L2 (the
-// cut, the maxima, the accumulators).
+// eighth of the segments each, added in order.  Bound by latency: two dependent
+// reads from L2 (the cut; the maxima with the accumulators), 5 to 6 us behind
+// the attention for 19 MB of segments; three blocks an SM (two: 2 us more for
+// b24, four, which spill: 4 us more).
 // ---------------------------------------------------------------------------
 constexpr int kJoinWarps = 8, kJoinThreads = 32 * kJoinWarps;
 constexpr int kFewSegments = 8;

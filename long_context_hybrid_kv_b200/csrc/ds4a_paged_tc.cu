@@ -10,20 +10,38 @@
 // cycles each): 0.95 us a tile; at 44 GB/s of HBM an SM its rows take 1.5 us.
 // 64 keys, not 128, leave room for nine 128-dim chunks of rows (2.25 tiles)
 // next to the 64 KiB of q^, so that the next tile is there and its first
-// product runs during this tile's softmax.
+// product runs during this tile's softmax.  What is left is the chain: a slot
+// of the ring is free after the second product, its new rows take about 1 us,
+// the first product, the softmax and the second product 0.6 + 1.1 + 0.6, and
+// the ring holds two tiles of that: 1.9 us a tile (FP8 2.6: the expansion of
+// the codes).  (A ring of 48-key tiles, or MMAs of two warps in turn, were
+// slower; integer expansion of the codes 114 us instead of 89.)
 //
-// Thread block (one per SM, 608 threads):
+// q^ and P are rounded to bf16, which the MMA takes (half a step, 2^-9, each,
+// which the softmax and the sum over keys average: 0.0026 of the output's
+// largest value against the 0.0017 of the output's own rounding); logits,
+// maxima, sums and O stay in float32.
+//
+// Thread block (one per SM, 640 threads):
 //   warps 0-7    q^ of every segment, softmax, epilogue: two warps per TMEM
 //                lane quarter with 32 heads each.  S^T of M = 64 has 16 keys
 //                in each quarter; a thread holds two keys x 8 heads of it, and
 //                later a dim row of O^T.
-//   warp 8       TMEM allocation; lane 0 issues the MMAs.
-//   warps 9-10   one key a thread, up to four tiles ahead: index, page, row
-//                address, and a prefetch of the row into L2, so that HBM keeps
-//                streaming while the ring is full.
+//   warp 8       TMEM allocation; an elected lane issues the MMAs.
+//   warps 9-10   find the segments and tell the others; one key a thread, up to
+//                four tiles ahead: index, page, row address, and a prefetch of
+//                the row into L2, so that HBM keeps streaming while the ring
+//                is full.
 //   warps 11-18  gather the rows by cp.async, a chunk (16 KiB) at a time, into
 //                a ring of nine, in the 128-byte swizzle.  FP8 rows go through
 //                registers, a tile ahead, and are expanded on the way.
+//   warp 19      fences landed chunks for the MMAs; angles and sinks of the
+//                segments to come.
+// Of a small call the prologue is half: code that runs once waits for its
+// instructions, so it is short and not unrolled (b1 x 64 entries 13.9 -> 11.4
+// us).  In a graph of calls with the window of 128: b1 x 8192 entries 21 us,
+// b32 x 1024 32 us, b32 x 8192 86 us (272 MB of rows: 3.2 TB/s), b256 x 512
+// selected 68 us.
 #include "ds4a_paged.cuh"
 #include "ds4a_tc.cuh"
 
