@@ -10,21 +10,24 @@
 // leave, in order.  Sources and destinations are disjoint, every row moves at
 // most once, and one entry in, one entry out moves a single row.
 //
-// evict_keep_kernel, one block per sequence of up to 32768 slots, a thread up
-// to 32 slots in a row: the budget-th largest weight by bisection over its
-// order-preserving integer form, the keys in registers (a count of all of them
-// is a few instructions a key and one barrier, without the contention that a
-// histogram of weights, which share their exponents, has; it ends as soon as a
-// bound leaves exactly `budget`), then two scans rank holes and movers.
+// evict_keep_kernel, one block or, for more than 16384 slots, a cluster of up
+// to eight per sequence, a thread up to 32 slots in a row: the budget-th
+// largest weight by bisection over its order-preserving integer form, the keys
+// in registers (a count of all of them is a few instructions a key and one
+// barrier, without the contention that a histogram of weights, which share
+// their exponents, has; it ends as soon as a bound leaves exactly `budget`),
+// then two scans rank holes and movers.  Bound by that chain of barriers: 9.4
+// us for 32 sequences of 1024 slots, 24 for 8 of 7596, 66 for 32 of 32768.
 // evict_select_kernel does the same by radix select from memory, for more
-// slots.  evict_move_kernel, over the whole GPU: the rows; few are moved by the
-// first kernel itself.
+// slots.  evict_move_kernel, over the whole GPU: the rows, bound by
+// memory; few are moved by the first kernel itself.
 #include "ds4a_evict.cuh"
 
 namespace ds4a {
 namespace {
 
 constexpr int kThreads = 1024;
+constexpr int kMaxTeam = 8;  // blocks of a cluster
 
 // larger = kept first; a protected entry is above all weights, NaN above the
 // others, -0 as 0
@@ -204,12 +207,43 @@ __device__ __forceinline__ void evict_move_row(const EvictArgs& a, int b, int fr
 }
 
 // kPer slots a thread
-template <int kPer>
+// The blocks of a cluster, each with its part of one sequence's slots.
+template <bool kMany>
+struct Team {
+  uint32_t rank = 0, size = 1;
+  __device__ Team() {
+    if (!kMany) return;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+    asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(size));
+  }
+  __device__ void sync() const {
+    if (kMany)
+      asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    else
+      __syncthreads();
+  }
+  // v into place `rank` of every block's array at (shared) at; one warp
+  __device__ void tell(const uint4* at, uint4 v) const {
+    const uint32_t r = threadIdx.x & 31;
+    if (r < size) {
+      const uint32_t here = (uint32_t)__cvta_generic_to_shared(at + rank);
+      asm volatile(
+          "{\n .reg .b32 there;\n mapa.shared::cluster.u32 there, %0, %1;\n"
+          " st.shared::cluster.v4.b32 [there], {%2, %3, %4, %5};\n}\n" ::"r"(here),
+          "r"(r), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+          : "memory");
+    }
+  }
+};
+
+template <int kPer, bool kMany>
 __global__ void __launch_bounds__(kThreads, 1) evict_keep_kernel(const EvictArgs a, int move_here) {
-  extern __shared__ unsigned int keys[];  // slot s at s + s / 32 (a thread's run of 32 would be one bank)
+  extern __shared__ unsigned int keys[];  // slot s of the block at s + s / 32 (a thread's run of 32 would be one bank)
   __shared__ int2 sums[kThreads / 32];
-  __shared__ int counts[2][kThreads / 32];
-  const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  __shared__ __align__(16) uint4 counts[2][kThreads / 32], told[2][kMaxTeam];
+  const Team<kMany> team;
+  const int b = blockIdx.x / team.size, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int all = kThreads * team.size, first = kThreads * kPer * team.rank;
   pdl_trigger();
   pdl_wait();
   const int pos = a.q_pos[b], gone = a.drop[b];
@@ -227,8 +261,10 @@ __global__ void __launch_bounds__(kThreads, 1) evict_keep_kernel(const EvictArgs
   const uint16_t* w = a.w ? a.w + (int64_t)b * a.w_stride : nullptr;
   const bool full = n > budget;
   const int oldest_kept = closed - a.recent;  // entries from here on are protected
+  const int n_here = min(kThreads * kPer, n - first);
 #pragma unroll 4
-  for (int s = tid; s < n; s += kThreads) {
+  for (int i = tid; i < n_here; i += kThreads) {
+    const int s = first + i;
     float x = acc[s];
     if (w) {
       x += bf2f(w[s]);
@@ -240,52 +276,114 @@ __global__ void __launch_bounds__(kThreads, 1) evict_keep_kernel(const EvictArgs
         e = s + gone;
         entry[s] = e;
       }
-      keys[s + (s >> 5)] = evict_key(x, e >= oldest_kept);
+      keys[i + (i >> 5)] = evict_key(x, e >= oldest_kept);
     }
   }
   if (!full) {
-    if (tid == 0) a.moves[b] = 0;
+    if (tid == 0 && team.rank == 0) a.moves[b] = 0;
     return;
   }
-  __syncthreads();
-  const int s0 = tid * kPer;
+  team.sync();  // (and every block of the cluster has begun)
+  const int i0 = tid * kPer, s0 = first + i0;
   unsigned int key[kPer];
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) key[i] = s0 + i < n ? keys[s0 + i + ((s0 + i) >> 5)] : 0u;
-  int round = 0;
-  auto count = [&](unsigned int bound) {  // keys >= bound (> 0), over the block
+  for (int i = 0; i < kPer; ++i) key[i] = s0 + i < n ? keys[i0 + i + ((i0 + i) >> 5)] : 0u;
+  // The largest bound that leaves `budget` keys or more; `above`: keys over it.
+  unsigned int bound = 0;
+  int above = 0, round = 0;
+  bool exact = false;
+  // One block: a bit a round.
+#pragma unroll 1
+  for (int shift = 31; shift >= 0 && !kMany && !exact; --shift) {
+    const unsigned int b2 = bound | (1u << shift);
     int c = 0;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) c += key[i] >= bound;
+    for (int i = 0; i < kPer; ++i) c += key[i] >= b2;
     c = __reduce_add_sync(0xffffffffu, c);
-    int* buf = counts[round++ & 1];
+    unsigned int* buf = reinterpret_cast<unsigned int*>(counts[round++ & 1]);
     if (lane == 0) buf[warp] = c;
     __syncthreads();
-    return __reduce_add_sync(0xffffffffu, buf[lane]);
-  };
-  // the largest bound that leaves `budget` keys or more; `above`: keys over it
-  unsigned int bound = 0;
-  int above = n;
-  bool exact = false;
-  for (int bit = 31; bit >= 0; --bit) {
-    const unsigned int b2 = bound | (1u << bit);
-    const int c = count(b2);
+    c = __reduce_add_sync(0xffffffffu, (int)buf[lane]);
     if (c >= budget) bound = b2;
     else above = c;
-    if (c == budget) {
-      exact = true;
-      break;
+    exact = c == budget;
+  }
+  // A cluster, whose rounds take longer: three bits a round, the keys at or
+  // over seven bounds counted at once, two counts of up to 32768 in a word.
+#pragma unroll 1
+  for (int shift = 30; shift >= 0 && kMany && !exact; shift -= 3) {
+    const unsigned int most = shift == 30 ? 3u : 7u;
+    unsigned int c[4] = {0, 0, 0, 0};  // bounds 1, 2 | 3, 4 | 5, 6 | 7
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      // how many of the bounds the key reaches
+      const unsigned int d = key[i] < bound ? 0u : min((key[i] - bound) >> shift, most);
+      c[0] += (d >= 1) | (d >= 2) << 16;
+      c[1] += (d >= 3) | (d >= 4) << 16;
+      c[2] += (d >= 5) | (d >= 6) << 16;
+      c[3] += d >= 7;
     }
+#pragma unroll
+    for (int q = 0; q < 4; ++q) c[q] = __reduce_add_sync(0xffffffffu, c[q]);
+    const int buf = round++ & 1;
+    if (lane == 0) counts[buf][warp] = make_uint4(c[0], c[1], c[2], c[3]);
+    __syncthreads();
+    const uint4 v = counts[buf][lane];
+    c[0] = __reduce_add_sync(0xffffffffu, v.x);
+    c[1] = __reduce_add_sync(0xffffffffu, v.y);
+    c[2] = __reduce_add_sync(0xffffffffu, v.z);
+    c[3] = __reduce_add_sync(0xffffffffu, v.w);
+    if (warp == 0) team.tell(told[buf], make_uint4(c[0], c[1], c[2], c[3]));
+    team.sync();
+    int k[7] = {0, 0, 0, 0, 0, 0, 0};
+#pragma unroll 1
+    for (uint32_t r = 0; r < team.size; ++r) {
+      const uint4 t = told[buf][r];
+      const unsigned int u[4] = {t.x, t.y, t.z, t.w};
+#pragma unroll
+      for (int q = 0; q < 7; ++q) k[q] += (int)(q & 1 ? u[q >> 1] >> 16 : u[q >> 1] & 0xFFFFu);
+    }
+    unsigned int j = 0;
+#pragma unroll
+    for (unsigned int q = 1; q <= 7; ++q)
+      if (q <= most) {
+        if (k[q - 1] >= budget) {
+          j = q;
+          exact = k[q - 1] == budget;
+        } else if (j == q - 1) {
+          above = k[q - 1];
+        }
+      }
+    bound += j << shift;
   }
   // a key above the bound is kept, of the equal ones the lowest `need`
-  const int need = exact ? 0x7FFFFFFF : budget - (above == n ? 0 : above);
-  int2 total;
+  const int need = exact ? 0x7FFFFFFF : budget - above;
+  // the sums of the blocks before this one, and of all
+  auto join = [&](int2 total, int2* before) {
+    *before = make_int2(0, 0);
+    if (!kMany) return total;
+    const int buf = round++ & 1;
+    if (warp == 0) team.tell(told[buf], make_uint4((unsigned)total.x, (unsigned)total.y, 0, 0));
+    team.sync();
+    int2 sum = make_int2(0, 0);
+#pragma unroll 1
+    for (uint32_t r = 0; r < team.size; ++r) {
+      const uint4 t = told[buf][r];
+      if (r == team.rank) *before = sum;
+      sum.x += (int)t.x;
+      sum.y += (int)t.y;
+    }
+    return sum;
+  };
+  int2 total, before;
   int ties = 0;
   if (!exact) {
     int mine = 0;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) mine += s0 + i < n && key[i] == bound;
     ties = block_scan(mine, 0, sums, &total).x;
+    join(total, &before);
+    ties += before.x;
   }
   unsigned int keep = 0;
   int holes = 0, movers = 0;
@@ -299,6 +397,9 @@ __global__ void __launch_bounds__(kThreads, 1) evict_keep_kernel(const EvictArgs
     movers += s >= budget && k;
   }
   int2 at = block_scan(holes, movers, sums, &total);
+  total = join(total, &before);
+  at.x += before.x;
+  at.y += before.y;
   int32_t* dst = a.list + (int64_t)b * 2 * budget;
   int32_t* src = dst + budget;
 #pragma unroll
@@ -309,22 +410,22 @@ __global__ void __launch_bounds__(kThreads, 1) evict_keep_kernel(const EvictArgs
     if (s < budget && !k) dst[at.x++] = s;
     if (s >= budget && k) src[at.y++] = s;
   }
-  __syncthreads();
+  team.sync();
   const int moved = total.y;
-  for (int r = tid; r < moved; r += kThreads) {
+  for (int r = kThreads * team.rank + tid; r < moved; r += all) {
     const int from = src[r], to = dst[r];
     acc[to] = acc[from];
     entry[to] = entry[from];
   }
   if (move_here)
-    for (int r = warp; r < moved; r += kThreads / 32) evict_move_row(a, b, src[r], dst[r]);
-  __syncthreads();
+    for (int r = (kThreads * team.rank + tid) / 32; r < moved; r += all / 32) evict_move_row(a, b, src[r], dst[r]);
+  team.sync();
   // slots behind the kept ones start over
-  for (int s = budget + tid; s < a.cap; s += kThreads) {
+  for (int s = budget + kThreads * team.rank + tid; s < a.cap; s += all) {
     acc[s] = 0.f;
     entry[s] = -1;
   }
-  if (tid == 0) {
+  if (tid == 0 && team.rank == 0) {
     a.moves[b] = moved;
     a.drop[b] = gone + (n - budget);
   }
@@ -340,14 +441,14 @@ __global__ void __launch_bounds__(256) evict_move_kernel(const EvictArgs a) {
   for (int r = blockIdx.x * 8 + (threadIdx.x >> 5); r < moves; r += gridDim.x * 8) evict_move_row(a, b, src[r], dst[r]);
 }
 
-template <int kPer>
-cudaError_t launch_keep(const EvictArgs& a, int move_here, cudaStream_t s) {
+template <int kPer, bool kMany>
+cudaError_t launch_keep(const EvictArgs& a, int team, int move_here, cudaStream_t s) {
   const int slots = kPer * kThreads, smem = (slots + slots / 32) * 4;
   static std::atomic<int> cache[kMaxDevices];
-  const cudaError_t e = ensure_smem(evict_keep_kernel<kPer>, smem, cache);
+  const cudaError_t e = ensure_smem(evict_keep_kernel<kPer, kMany>, smem, cache);
   if (e != cudaSuccess) return e;
   TraceScope tr("evict_keep", s);
-  return launch_pdl(evict_keep_kernel<kPer>, dim3(a.B), dim3(kThreads), smem, s, a, move_here);
+  return launch_pdl_cluster(evict_keep_kernel<kPer, kMany>, dim3(a.B * team), dim3(kThreads), smem, s, team, a, move_here);
 }
 
 }  // namespace
@@ -355,14 +456,28 @@ cudaError_t launch_keep(const EvictArgs& a, int move_here, cudaStream_t s) {
 cudaError_t launch_evict(const EvictArgs& a, cudaStream_t s) {
   const int most = min(a.budget, a.cap - a.budget);  // rows that a sequence may move
   const int move_here = most <= 64;                  // two rows a warp: less than a launch
-  const int per = (a.cap + kThreads - 1) / kThreads;
+  // A thread of one block holds up to 16 slots; above that a cluster, whose
+  // rounds take longer, pays: until a thread has four or all SMs have a block
+  // (32 sequences of 32768 slots, one block and four: 91 and 66 us; of 16384:
+  // 36 and 38).  A large batch has one block a sequence.
+  int team = 1;
+  while (team < kMaxTeam && a.cap > 16 * kThreads && (int64_t)team * 4 * kThreads < a.cap && (int64_t)a.B * team * 2 <= 148)
+    team *= 2;
+  const int per = (a.cap + kThreads * team - 1) / (kThreads * team);
   cudaError_t e;
-  if (per <= 1) e = launch_keep<1>(a, move_here, s);
-  else if (per <= 4) e = launch_keep<4>(a, move_here, s);
-  else if (per <= 8) e = launch_keep<8>(a, move_here, s);
-  else if (per <= 16) e = launch_keep<16>(a, move_here, s);
-  else if (per <= 32) e = launch_keep<32>(a, move_here, s);
-  else {
+  if (team == 1) {
+    if (per <= 1) e = launch_keep<1, false>(a, team, move_here, s);
+    else if (per <= 4) e = launch_keep<4, false>(a, team, move_here, s);
+    else if (per <= 8) e = launch_keep<8, false>(a, team, move_here, s);
+    else if (per <= 16) e = launch_keep<16, false>(a, team, move_here, s);
+    else if (per <= 32) e = launch_keep<32, false>(a, team, move_here, s);
+  } else {
+    if (per <= 4) e = launch_keep<4, true>(a, team, move_here, s);
+    else if (per <= 8) e = launch_keep<8, true>(a, team, move_here, s);
+    else if (per <= 16) e = launch_keep<16, true>(a, team, move_here, s);
+    else if (per <= 32) e = launch_keep<32, true>(a, team, move_here, s);
+  }
+  if (per > 32) {
     TraceScope tr("evict_select", s);
     e = launch_pdl(evict_select_kernel, dim3(a.B), dim3(kThreads), 0, s, a);
   }

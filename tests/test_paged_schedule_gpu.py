@@ -8,10 +8,16 @@ import pytest
 import torch
 
 import long_context_hybrid_kv_b200 as L
-from gpu_util import check_ok, i32
-from test_paged_gpu import Case, _evict_case
+import paged_ref as P
+from gpu_util import bf, bits, check_ok, f32, i32
+from oracle import ds4a_oracle as O
+from test_paged_gpu import Case
 
 pytestmark = pytest.mark.gpu
+
+
+def bf_bits(x):
+    return torch.from_numpy(np.asarray(x, np.float32)).bfloat16().view(torch.int16).numpy().view(np.uint16)
 
 
 def spread(name, lens, weights=True, **kw):
@@ -90,10 +96,48 @@ def test_generic_shape_of_many_sequences():
     spread("generic", lens, H=3, D=64, R=16, W=8, page=7)
 
 
-@pytest.mark.parametrize("cap", [1024, 1025, 4096, 8192, 8193, 16384, 32768, 32769])
-def test_evict_every_size_of_cache(cap):
-    # a block's threads hold 1, 4, 8, 16 or 32 slots each; above that two launches
-    _evict_case(f"size{cap}", [cap, cap - 1, cap // 2 + 1], cap, cap // 2, 7, 32)
+def evict_many(name, B, cap, budget, recent, D=32, page=40):
+    """A batch of caches of unequal lengths, weights with ties, small rows."""
+    rng = np.random.default_rng(sum(map(ord, name)))
+    m, per = 4, -(-cap // page)
+    cfg = L.LayerCfg(2, D, 0, 0, 64, 128, 16, m, D ** -0.5, 10000.0, 1e-6)
+    table = rng.permutation(B * per + 1)[:B * per].reshape(B, per).astype(np.int32)
+    pages = rng.integers(0, 60000, (B * per + 1, page, D)).astype(np.uint16)
+    lens = [cap, budget + 1, budget] + [int(v) for v in rng.integers(budget // 2, cap + 1, max(0, B - 3))]
+    lens = lens[:B]
+    acc = (rng.integers(0, 64, (B, cap)) / 8).astype(np.float32)  # many ties
+    acc[0] = rng.random(cap)
+    entry, drop = np.full((B, cap), -1, np.int32), np.zeros(B, np.int32)
+    w = bf_bits(rng.random((B, cap)))
+    pos = np.asarray([n * m + 1 for n in lens], np.int32)
+    d_pages, d_w, d_table = bf(pages), bf(w), i32(table)
+    kv = L.paged_kv(d_pages, d_table, page)
+    d_acc, d_entry, d_drop = f32(acc), i32(entry), i32(drop)
+    ws = torch.full((L.ds4a_paged_evict_workspace(kv, B),), 0xFF, dtype=torch.uint8, device="cuda")
+    L.ds4a_paged_evict(cfg, kv, i32(pos), budget, recent, d_acc, d_entry, d_drop, ws, weights=d_w)
+    check_ok()
+    for b, n in enumerate(lens):
+        acc[b], entry[b], drop[b], moves = P.evict(O.widen(w[b]), acc[b], entry[b], 0, n, n, budget, recent)
+        if len(moves):
+            fr, to = np.asarray(moves).T
+            pages[table[b][to // page], to % page] = pages[table[b][fr // page], fr % page]
+    assert np.array_equal(d_drop.cpu().numpy(), drop)
+    assert np.array_equal(d_entry.cpu().numpy(), entry)
+    assert np.array_equal(d_acc.cpu().numpy(), acc)
+    assert np.array_equal(bits(d_pages), pages)
+
+
+# a cluster of 1 to 8 blocks a sequence, 1 to 32 slots a thread
+@pytest.mark.parametrize("B,cap", [(3, 1024), (3, 1025), (3, 4096), (1, 4097), (3, 8193), (2, 16385), (1, 40000), (2, 100000),
+                                   (1, 200001), (40, 9000), (38, 30000), (75, 1030), (80, 5000), (80, 9000), (76, 20000)])
+def test_evict_every_size_of_cache(B, cap):
+    evict_many(f"size{B}.{cap}", B, cap, cap // 2, 7)
+    evict_many(f"few{B}.{cap}", B, cap, cap - 3, cap // 3)
+
+
+def test_evict_more_slots_than_a_cluster_holds():
+    evict_many("huge", 1, 262150, 262000, 100)
+    evict_many("half", 1, 300000, 150000, 100)
 
 
 def test_binding_refuses_other_devices_and_sizes():
