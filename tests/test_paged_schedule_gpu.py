@@ -58,6 +58,47 @@ def test_more_items_than_blocks_share_them(fp8):
     spread(f"share{fp8}", lens, H=6, fp8=fp8, page=16)
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("B,most", [(2500, 4), (900, 260)])
+def test_many_segments_a_block(B, most, fp8):
+    # 6 to 17 whole items one after the other in every block
+    lens = [int(v) for v in np.random.default_rng(B).integers(0, most, B)]
+    c = Case(f"segs{B}{fp8}", lens, 16, m=16, H=2, W=4, fp8=fp8, spare=0)
+    c.run()
+    check_ok()
+    got = c.out.double().cpu().numpy()
+    for b in list(range(0, B, 13)) + [B - 1]:
+        out, _, bound, _ = c.ref(b)
+        assert (np.abs(got[b] - out) <= bound).all(), b
+
+
+def test_more_sequences_than_the_schedule_keeps():
+    # lengths behind the first 36864 are computed where they are needed
+    B = 37000
+    rng = np.random.default_rng(8)
+    cfg = L.LayerCfg(1, 512, 64, 2, 64, 128, 512, 16, 512 ** -0.5, 10000.0, 1e-6)
+    pages = rng.standard_normal((64, 4, 512)).astype(np.float32)
+    table = rng.integers(0, 64, (B, 1)).astype(np.int32)  # attention may share pages
+    n = rng.integers(0, 5, B)
+    pos = (n * 16 + rng.integers(0, 15, B)).astype(np.int32)
+    q, win = rng.standard_normal((B, 1, 512)).astype(np.float32), rng.standard_normal((B, 2, 512)).astype(np.float32)
+    bfc = lambda x: torch.from_numpy(x).bfloat16().cuda()  # noqa: E731
+    d_pages, d_table, d_q, d_win = bfc(pages), i32(table), bfc(q), bfc(win)
+    kv = L.paged_kv(d_pages, d_table, 4)
+    out = torch.full((B, 1, 512), 7.0, dtype=torch.bfloat16, device="cuda")
+    ws = torch.empty(L.ds4a_paged_attend_workspace(cfg, kv, B), dtype=torch.uint8, device="cuda")
+    L.ds4a_paged_attend(cfg, kv, i32(pos), d_q, torch.ones(512, device="cuda"), d_win, 2, torch.zeros(1, device="cuda"), out, ws)
+    check_ok()
+    got = out.double().cpu().numpy()
+    dp, dq, dw = (t.double().cpu().numpy() for t in (d_pages, d_q, d_win))
+    for b in list(range(0, B, 501)) + [36863, 36864, 36865, B - 1]:
+        p = int(pos[b])
+        near = np.arange(max(0, p - 1), p + 1) % 2
+        rows = np.concatenate([dp[table[b, 0]][:n[b]], dw[b][near]])
+        ref, _, bound, _ = P.attend(dq[b], np.ones(512), rows, int(n[b]), np.zeros(1), p, 512 ** -0.5, 64, 10000.0, 1e-6)
+        assert (np.abs(got[b] - ref) <= bound).all(), b
+
+
 def test_more_items_than_blocks_by_head_groups():
     # 80 sequences x 2 groups of heads
     lens = [int(v) for v in np.random.default_rng(4).integers(0, 500, 80)]
