@@ -563,6 +563,8 @@ int ds4a_paged_evict(const ds4a_layer_cfg* cfg, const ds4a_paged_kv* kv, int B, 
  *           K / 128 blocks of a row range lie side by side, row ranges follow
  *           one another; the last is padded to 128 rows
  * (the order in which the tensor core takes them).  K a multiple of 128.
+ * A matrix may be quantised and used by ds4a_out_proj_mxfp4 in the next call
+ * on the same stream: the quantiser orders fully.
  */
 /* Bytes of the scales of a rows x K matrix (0: bad arguments). */
 size_t ds4a_mxfp4_scale_bytes(int rows, int K);

@@ -710,7 +710,7 @@ int ds4a_quantize_mxfp4(int n_rows, int K, const ds4a_bf16* in, int64_t in_strid
   if (n_rows == 0) return DS4A_OK;
   if (!in || !codes || !scales || !aligned16(in) || !aligned16(codes) || !aligned16(scales)) return DS4A_EINVAL;
   if (in_stride < K || in_stride % 8 != 0) return DS4A_EINVAL;
-  return cuda_rc(launch_quantize_mxfp4(n_rows, K, in, in_stride, codes, scales, (cudaStream_t)stream));
+  return cuda_rc(launch_quantize_mxfp4(n_rows, K, in, in_stride, codes, scales, false, (cudaStream_t)stream));
 }
 
 static int check_oproj_mxfp4(const ds4a_oproj_cfg* c) {
@@ -772,7 +772,7 @@ int ds4a_out_proj_mxfp4(const ds4a_oproj_cfg* cfg, int M, const ds4a_bf16* o, co
   if (!err) return DS4A_ECUDA;
   Mxfp4Product p;
   p.o = mxfp4_small(M) ? o : nullptr;  // few rows: the first product quantises them itself
-  if (!p.o && launch_quantize_mxfp4(M, k, o, k, w.o_codes, w.o_scales, s) != cudaSuccess) return DS4A_ECUDA;
+  if (!p.o && launch_quantize_mxfp4(M, k, o, k, w.o_codes, w.o_scales, true, s) != cudaSuccess) return DS4A_ECUDA;
   p.M = M; p.N = n1; p.K = k1; p.n_per_group = cfg->group_rank; p.a_cols = k;
   p.a_codes = w.o_codes; p.a_scales = w.o_scales; p.b_codes = wa_codes; p.b_scales = wa_scales;
   p.y = nullptr; p.q_codes = w.mid_codes; p.q_scales = w.mid_scales; p.part = w.part; p.err = err;

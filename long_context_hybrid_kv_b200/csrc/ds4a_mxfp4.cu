@@ -82,10 +82,14 @@ __device__ __forceinline__ int mx_block_words(const uint4 (&u)[4], uint4* codes)
 }
 
 // A thread a 32-value block.  64 bytes in, 16.5 out: bound by HBM (16384 x
-// 32768 values in 223 us, 6.1 TB/s).
+// 32768 values in 223 us, 6.1 TB/s).  kEarly: the next kernel may start while
+// this one runs.  Only for a next kernel that waits before it reads the result:
+// the products load their weights before they wait, so a matrix that may become
+// a weight is quantised without it, and the next kernel starts when it is done.
+template <bool kEarly>
 __global__ void __launch_bounds__(256) quantize_mxfp4_kernel(int n_rows, int rows_pad, int K, const uint16_t* in,
                                                              int64_t in_stride, uint8_t* codes, uint8_t* scales) {
-  pdl_trigger();
+  if (kEarly) pdl_trigger();
   pdl_wait();
   const int kb = K / kMxBlock;
   const int64_t n = (int64_t)rows_pad * kb;
@@ -241,8 +245,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t s = kt % kStages, dst = sbase + s * kStageBytes, full = bar(kFull + s);
           if (kt >= (uint32_t)kStages && !mbar_wait(bar(kEmpty + s), (kt / kStages - 1) & 1u, abort_flag, err)) break;
           mbar_expect_tx(full, kStageBytes);
-          // the weights are an input: the first stages' come while the
-          // kernel before this one ends
+          // the weights are an input (their quantiser lets no kernel start
+          // before it is done): the first stages' come while the kernel
+          // before this one ends
           tma_load_2d(dst + kStageA, &bmap, k * (kBK / 2), w.n0, full);
           const uint8_t* sb = p.b_scales + ((int64_t)(w.n0 / 128) * p.b_blocks + 2 * k) * 512;
           bulk_g2s(dst + kOffSB, sb, 1024, full);
@@ -677,12 +682,13 @@ cudaError_t launch_gemm_kernel(const CUtensorMap& amap, const CUtensorMap& bmap,
 }  // namespace
 
 cudaError_t launch_quantize_mxfp4(int n_rows, int K, const uint16_t* in, int64_t in_stride, uint8_t* codes,
-                                  uint8_t* scales, cudaStream_t s) {
+                                  uint8_t* scales, bool early, cudaStream_t s) {
   const int pad = (n_rows + 127) / 128 * 128;
   const int64_t blocks = ((int64_t)pad * (K / kMxBlock) + 255) / 256;
   const int grid = (int)(blocks < 148 * 8 ? blocks : 148 * 8);
   TraceScope tr("quantize_mxfp4", s);
-  return launch_pdl(quantize_mxfp4_kernel, dim3(grid), dim3(256), 0, s, n_rows, pad, K, in, in_stride, codes, scales);
+  return launch_pdl(early ? quantize_mxfp4_kernel<true> : quantize_mxfp4_kernel<false>, dim3(grid), dim3(256), 0, s,
+                    n_rows, pad, K, in, in_stride, codes, scales);
 }
 
 // Few rows cannot fill the SMs with tiles; K is then split until they do, as

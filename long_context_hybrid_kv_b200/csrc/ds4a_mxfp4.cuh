@@ -22,9 +22,11 @@ __host__ __device__ constexpr int64_t mxfp4_scale_at(int64_t row, int64_t block,
 }
 
 // bf16 rows -> codes and scales; padding rows of the last block of 128 get
-// zero scales
+// zero scales.  early: the next kernel of the stream may start before they are
+// written (it has to wait before it reads them, as the products do for A, but
+// not for their weights)
 cudaError_t launch_quantize_mxfp4(int n_rows, int K, const uint16_t* in, int64_t in_stride, uint8_t* codes,
-                                  uint8_t* scales, cudaStream_t s);
+                                  uint8_t* scales, bool early, cudaStream_t s);
 
 // One grouped product: outputs n of group j = n / n_per_group take the
 // columns j * K .. (j + 1) * K of A's a_cols.  The result goes out as bf16
