@@ -99,7 +99,7 @@ __device__ __forceinline__ int closing_entry(const CompressArgs& a, int b, int p
     if (report) raise_err(a.err, DS4A_DEV_BAD_INDEX);
     return -1;
   }
-  if (a.pg_table != nullptr) {
+  if (a.pg_size != 0) {
     *row = page_row(a, b, i);
     if (*row < 0) {
       if (report) raise_err(a.err, DS4A_DEV_BAD_INDEX);
@@ -112,11 +112,11 @@ __device__ __forceinline__ int closing_entry(const CompressArgs& a, int b, int p
 // First element of entry i of sequence b in the bf16 pool, and its byte row
 // in a block-scaled one (row: as closing_entry gave it).
 __device__ __forceinline__ uint16_t* entry_dst(const CompressArgs& a, int b, int i, int64_t row) {
-  return a.pool + (a.pg_table != nullptr ? row * a.c : (int64_t)b * a.pool_bstride + (int64_t)i * a.c);
+  return a.pool + (a.pg_size != 0 ? row * a.c : (int64_t)b * a.pool_bstride + (int64_t)i * a.c);
 }
 __device__ __forceinline__ uint8_t* entry_dst_mx(const CompressArgs& a, int b, int i, int64_t row) {
   return a.qpool +
-         (a.pg_table != nullptr ? row * a.q_row : (int64_t)b * a.q_bstride + (int64_t)i * a.q_row);
+         (a.pg_size != 0 ? row * a.q_row : (int64_t)b * a.q_bstride + (int64_t)i * a.q_row);
 }
 
 // Append mode: store the new token's rows of every stream (position p >= 0)

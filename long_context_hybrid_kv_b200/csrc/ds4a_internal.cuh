@@ -238,8 +238,9 @@ struct CompressArgs {
   int64_t q_bstride, q_row;
   uint8_t* qscales;
   int64_t qs_bstride;
-  // paged output (pg_table != nullptr, append mode): entry i of sequence b
-  // goes to slot i - pg_drop[b] of its pages, rows counted from pool / qpool
+  // paged output (pg_size != 0, append mode): entry i of sequence b goes to
+  // slot i - pg_drop[b] of its pages, rows counted from pool / qpool; with
+  // pg_cap 0 (then pg_table may be null) there is no slot
   const int32_t* pg_table;
   int64_t pg_stride;
   const int32_t* pg_drop;  // nullable
