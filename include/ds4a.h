@@ -509,7 +509,8 @@ int ds4a_paged_attend(const ds4a_layer_cfg* cfg, const ds4a_paged_kv* kv, int B,
 /*
  * ds4a_paged_append -- ds4a_compress_append(_mx) into a paged cache: the
  * entry i that a token closes goes to slot i - drop[b].  c = cfg->head_dim
- * channels; kv->format 0 or DS4A_MX_KV_FP8.  A slot at or behind max_pages *
+ * channels; kv->format 0 or DS4A_MX_KV_FP8 (then norm_g must be given, unless
+ * cfg->rope_dim is 0: DS4A_EUNSUPPORTED).  A slot at or behind max_pages *
  * page_size, a negative slot or a bad page is recorded as
  * DS4A_DEV_BAD_INDEX and the entry is not stored (its rows still enter the
  * state).

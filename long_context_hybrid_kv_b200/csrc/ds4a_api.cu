@@ -644,9 +644,11 @@ int ds4a_paged_append(const ds4a_layer_cfg* cfg, const ds4a_paged_kv* kv, int B,
                       const ds4a_bf16* zb, const float* bias_a, const float* bias_b, const float* norm_g,
                       ds4a_bf16* state, ds4a_stream stream) {
   if (check_cfg(cfg) != DS4A_OK) return DS4A_EINVAL;
-  const int c = cfg->head_dim, R = norm_g ? cfg->rope_dim : 0;
-  if (const int rc = check_kv(kv, c, R)) return rc;
+  const int c = cfg->head_dim;
+  if (const int rc = check_kv(kv, c, cfg->rope_dim)) return rc;
   if (!aligned16(drop)) return DS4A_EINVAL;
+  // an FP8 row keeps cfg->rope_dim dims in bf16; without a norm the compressor rotates, and so keeps, none
+  if (kv->format == DS4A_MX_KV_FP8 && !norm_g && cfg->rope_dim != 0) return DS4A_EUNSUPPORTED;
   const int fmt = kv->format == DS4A_MX_KV_FP8 ? 1 : 0;
   // every entry number may come: the slot is checked on the device
   CompressArgs a;

@@ -132,6 +132,14 @@ def test_append_refuses(bad):
     assert append(**bad) == L.DS4A_EINVAL
 
 
+def test_append_refuses_fp8_rows_without_a_norm():
+    # (their RoPE dims are bf16, which an entry without norm and rotation does not have)
+    k = kv(format=L.DS4A_MX_KV_FP8)
+    assert append(k=k, g=None) == L.DS4A_EUNSUPPORTED
+    assert append(k=k, g=None, cb=A, zb=A, bb=A) == L.DS4A_EUNSUPPORTED
+    assert append(k=k, g=None, B=0, c=cfg(rope_dim=0)) == L.DS4A_OK
+
+
 def test_append_empty():
     assert append(B=0) == L.DS4A_OK
 
