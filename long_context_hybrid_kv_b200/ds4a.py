@@ -485,9 +485,7 @@ def ds4a_paged_append(cfg: LayerCfg, kv: PagedKv, pos, ca, za, bias_a, state, *,
     B, c = ca.shape
     if c != cfg.head_dim:
         raise ValueError("a paged cache holds K=V entries of head_dim channels")
-    _kv_of(kv, B, dev)
-    if norm_g is not None:  # (RoPE, and FP8 rows, come with the norm)
-        _row_of(cfg, kv)
+    _kv_of(kv, B, dev), _row_of(cfg, kv)
     some = lambda t, dtype, n, name: None if t is None else _flat(t, dtype, n, name, dev)  # noqa: E731
     need = ds4a_compress_state_bytes(cfg, B, c, cb is not None)
     if state.get_device() != dev or not state.is_contiguous() or state.numel() * state.element_size() < need:

@@ -140,6 +140,18 @@ def test_append_refuses_fp8_rows_without_a_norm():
     assert append(k=k, g=None, B=0, c=cfg(rope_dim=0)) == L.DS4A_OK
 
 
+@pytest.mark.parametrize("norm", [False, True])
+def test_binding_checks_the_rows_that_append_writes(norm):
+    table = torch.zeros((2, 2), dtype=torch.int32)
+    x = torch.zeros((2, 512), dtype=torch.bfloat16)
+    state = torch.zeros(L.ds4a_compress_state_bytes(cfg(), 2, 512, False), dtype=torch.uint8)
+    g = torch.ones(512) if norm else None
+    pos, bias = torch.zeros(2, dtype=torch.int32), torch.zeros((4, 512))
+    for pages, fmt in ((torch.zeros((4, 16, 256), dtype=torch.bfloat16), 0), (torch.zeros((4, 16, 528), dtype=torch.uint8), 1)):
+        with pytest.raises(ValueError, match="rows must have"):
+            L.ds4a_paged_append(cfg(), L.paged_kv(pages, table, 16, fmt=fmt), pos, x, x, bias, state, norm_g=g, stream=0)
+
+
 def test_append_empty():
     assert append(B=0) == L.DS4A_OK
 
