@@ -498,7 +498,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
           inv_s[st] = den > 0.f ? 1.f / den : 0.f;
           if (a.weights) a.lse2[(int64_t)sg.item * kH + st] = den > 0.f ? m + log2f(den) : sink_t[st];
         } else {
-          part[st] = m <= kNoRef ? -INFINITY : m * 0.6931471805599453f;  // natural-log units
+          // natural-log units; -inf: no key counts.  (A head whose logits are
+          // all NaN has no reference either: its sum, NaN, is handed on.)
+          part[st] = m <= kNoRef && l == 0.f ? -INFINITY : m * 0.6931471805599453f;
           part[kH + st] = l;
         }
       }

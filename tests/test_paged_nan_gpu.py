@@ -1,0 +1,77 @@
+"""NaN and infinity in what decode attention over the paged cache reads: they
+must show in exactly the outputs that they reach, however a batch is spread
+over the GPU."""
+import numpy as np
+import pytest
+import torch
+
+import long_context_hybrid_kv_b200 as L
+from gpu_util import check_ok
+from test_paged_gpu import Case
+
+pytestmark = pytest.mark.gpu
+
+NAN, INF = 0x7FC0, 0x7F80  # bf16
+
+# finished in one block; cut into pieces of a block each (of few and of many
+# segments); the row of all tiles cut into ranges; whole items that share blocks
+SPREADS = {"whole": [100, 30], "pieces": [5000, 300], "few pieces": [700] * 40, "ranges": [400] * 152,
+           "shared": [120] * 300}
+KINDS = {"bf16": dict(H=5), "fp8": dict(H=5, fp8=True), "two groups": dict(H=70)}
+
+
+def twice(name, lens, change, **kw):
+    """The outputs before and after change(case, sequence): (out, weights) each."""
+    c = Case(name, lens, 64, m=16, spare=0, **kw)
+    w = torch.full((c.B, max(lens)), 7.0, dtype=torch.bfloat16, device="cuda")
+    ws = c.workspace(weights=True)
+    got = []
+    for i in range(2):
+        if i:
+            change(c)
+        c.out.fill_(7.0), w.fill_(7.0)
+        c.run(weights=w, ws=ws)
+        check_ok()
+        got.append((c.out.clone(), w.clone()))
+    return c, got[0], got[1]
+
+
+def same(a, b):
+    return torch.equal(a.view(torch.int16), b.view(torch.int16))
+
+
+def reached(c, first, then, b, heads):
+    """Sequence b's outputs of `heads` and its slots' weights are NaN, all else has the same bits."""
+    hit = torch.zeros((c.B, c.H), dtype=torch.bool, device="cuda")
+    hit[b, heads] = True
+    assert torch.isnan(then[0][hit]).all(), "outputs that are not NaN"
+    assert same(first[0][~hit], then[0][~hit]), "other outputs changed"
+    assert torch.isfinite(first[0]).all()
+    slots = torch.zeros((c.B, then[1].shape[1]), dtype=torch.bool, device="cuda")
+    slots[b, :c.lens[b]] = True
+    assert torch.isnan(then[1][slots]).all(), "weights that are not NaN"
+    assert same(first[1][~slots], then[1][~slots]), "other weights changed"
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("spread", SPREADS)
+def test_nan_in_a_query(kind, spread):
+    nan_query(kind, spread, NAN)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("spread", ["whole", "pieces"])
+def test_infinity_in_a_query(kind, spread):
+    # (its root mean square is infinite: infinity times 0)
+    nan_query(kind, spread, INF)
+
+
+def nan_query(kind, spread, value):
+    lens = SPREADS[spread]
+    b, h = len(lens) // 2 - 1, KINDS[kind]["H"] - 1
+
+    def change(c):
+        c.d_q.view(torch.int16)[b, h, 6] = value
+
+    c, first, then = twice(f"nq{kind}{spread}", lens, change, **KINDS[kind])
+    reached(c, first, then, b, [h])
