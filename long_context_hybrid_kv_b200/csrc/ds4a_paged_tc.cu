@@ -493,14 +493,14 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
       float* part = paged_part(a, blockIdx.x, sg.slot);
       if (st < kH) {
         const float l = red[st] + red[64 + st] + red[128 + st] + red[192 + st], m = mrun[st];
+        // (a head whose logits are all NaN has no reference either: its sum, NaN, is handed on)
+        const bool none = m <= kNoRef && l == 0.f;  // no key counts
         if (sg.whole) {
-          const float den = m <= kNoRef ? 0.f : l + exp2f(sink_t[st] - m);
-          inv_s[st] = den > 0.f ? 1.f / den : 0.f;
-          if (a.weights) a.lse2[(int64_t)sg.item * kH + st] = den > 0.f ? m + log2f(den) : sink_t[st];
+          const float den = l + exp2f(sink_t[st] - m);
+          inv_s[st] = none ? 0.f : 1.f / den;
+          if (a.weights) a.lse2[(int64_t)sg.item * kH + st] = none ? sink_t[st] : m + log2f(den);
         } else {
-          // natural-log units; -inf: no key counts.  (A head whose logits are
-          // all NaN has no reference either: its sum, NaN, is handed on.)
-          part[st] = m <= kNoRef && l == 0.f ? -INFINITY : m * 0.6931471805599453f;
+          part[st] = none ? -INFINITY : m * 0.6931471805599453f;  // natural-log units
           part[kH + st] = l;
         }
       }

@@ -75,3 +75,40 @@ def nan_query(kind, spread, value):
 
     c, first, then = twice(f"nq{kind}{spread}", lens, change, **KINDS[kind])
     reached(c, first, then, b, [h])
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("spread", SPREADS)
+@pytest.mark.parametrize("all_rows", [False, True])
+def test_nan_in_rows_in_use(kind, spread, all_rows):
+    """One row of a sequence, or all of its cache's (pieces then hold nothing else)."""
+    lens = SPREADS[spread]
+    b = len(lens) // 2 - 1
+
+    def change(c):
+        n = c.lens[b]
+        s = torch.arange(n, device="cuda") if all_rows else torch.tensor([n // 3], device="cuda")
+        at = c.d_table[b].long()[s // 64], s % 64
+        if c.fp8:
+            c.pages[at[0], at[1], 3] = 0x7F  # the code of NaN
+        else:
+            c.pages.view(torch.int16)[at[0], at[1], 3] = NAN
+
+    c, first, then = twice(f"nr{kind}{spread}{all_rows}", lens, change, **KINDS[kind])
+    reached(c, first, then, b, list(range(c.H)))
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("spread", SPREADS)
+def test_nan_in_a_sink(kind, spread):
+    h = KINDS[kind]["H"] - 2
+
+    def change(c):
+        c.d_sink[h] = float("nan")
+
+    c, first, then = twice(f"ns{kind}{spread}", SPREADS[spread], change, **KINDS[kind])
+    assert torch.isnan(then[0][:, h]).all()
+    keep = [i for i in range(c.H) if i != h]
+    assert same(first[0][:, keep], then[0][:, keep])
+    for b, n in enumerate(c.lens):
+        assert torch.isnan(then[1][b, :n]).all() and same(first[1][b, n:], then[1][b, n:])
