@@ -11,6 +11,7 @@ constexpr int kGenThreads = 256;
 constexpr int kGenHeads = 8;   // heads of an item
 constexpr int kGenKeys = 32;   // keys of a tile: 8 heads x 32 keys, one logit a thread
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kNoMax = -1e30f;  // maximum of a segment whose logits are all NaN: finite, below any logit
 
 // dims d, d + 1 of a cache row
 __device__ __forceinline__ float2 row_pair(const PagedArgs& a, const uint8_t* row, bool fp8, int d) {
@@ -109,8 +110,9 @@ __global__ void __launch_bounds__(kGenThreads) paged_attend_generic_kernel(const
       float mt = z;
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, o));
+      // (the maximum passes NaN over, the probabilities and their sum do not)
       const float mo = ml[warp], mn = fmaxf(mo, mt);
-      const float p = mn == -INFINITY ? 0.f : exp2f(z - mn);
+      const float p = exp2f(z - (mn == -INFINITY ? 0.f : mn));
       const float l = warp_sum(p);
       ps[warp * kGenKeys + lane] = p;
       __syncwarp();
@@ -137,12 +139,12 @@ __global__ void __launch_bounds__(kGenThreads) paged_attend_generic_kernel(const
     if (sg.whole) {
       // finished here: the sink joins the denominator, the rope slice turns back
       if (tid < nh) {
-        const float mx = ml[tid] / kLog2e;
-        const float den = ml[tid] == -INFINITY ? 0.f : ml[kGenHeads + tid] + expf(a.sink[hb + tid] - mx);
-        ml[2 * kGenHeads + tid] = den > 0.f ? 1.f / den : 0.f;
+        const float mx = ml[tid] / kLog2e, l = ml[kGenHeads + tid];
+        const bool none = ml[tid] == -INFINITY && l == 0.f;  // no key counts
+        const float den = l + expf(a.sink[hb + tid] - mx);
+        ml[2 * kGenHeads + tid] = none ? 0.f : 1.f / den;
         if (a.weights)
-          a.lse2[(int64_t)sg.item * kGenHeads + tid] =
-              den > 0.f ? ml[tid] + log2f(den) : a.sink[hb + tid] * kLog2e;
+          a.lse2[(int64_t)sg.item * kGenHeads + tid] = none ? a.sink[hb + tid] * kLog2e : ml[tid] + log2f(den);
       }
       __syncthreads();
 #pragma unroll
@@ -166,8 +168,10 @@ __global__ void __launch_bounds__(kGenThreads) paged_attend_generic_kernel(const
     } else {
       float* part = paged_part(a, blockIdx.x, sg.slot);
       if (tid < kGenHeads) {
-        part[tid] = ml[tid] / kLog2e;  // -inf stays
-        part[kGenHeads + tid] = ml[kGenHeads + tid];
+        // -inf stays, unless the logits are all NaN: -inf says that no key counts
+        const float l = ml[kGenHeads + tid];
+        part[tid] = ml[tid] == -INFINITY && l != 0.f ? kNoMax : ml[tid] / kLog2e;
+        part[kGenHeads + tid] = l;
       }
 #pragma unroll
       for (int i = 0; i < kAcc; ++i) {

@@ -17,7 +17,8 @@ NAN, INF = 0x7FC0, 0x7F80  # bf16
 # segments); the row of all tiles cut into ranges; whole items that share blocks
 SPREADS = {"whole": [100, 30], "pieces": [5000, 300], "few pieces": [700] * 40, "ranges": [400] * 152,
            "shared": [120] * 300}
-KINDS = {"bf16": dict(H=5), "fp8": dict(H=5, fp8=True), "two groups": dict(H=70)}
+KINDS = {"bf16": dict(H=5), "fp8": dict(H=5, fp8=True), "two groups": dict(H=70),
+         "generic": dict(H=3, D=64, R=16, W=8)}
 
 
 def twice(name, lens, change, **kw):
