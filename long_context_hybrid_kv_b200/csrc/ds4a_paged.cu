@@ -144,7 +144,7 @@ __global__ void __launch_bounds__(kGenThreads) paged_attend_generic_kernel(const
         const float den = l + expf(a.sink[hb + tid] - mx);
         ml[2 * kGenHeads + tid] = none ? 0.f : 1.f / den;
         if (a.weights)
-          a.lse2[(int64_t)sg.item * kGenHeads + tid] = none ? a.sink[hb + tid] * kLog2e : ml[tid] + log2f(den);
+          a.lse2[(int64_t)sg.item * kGenHeads + tid] = none ? INFINITY : ml[tid] + log2f(den);
       }
       __syncthreads();
 #pragma unroll
@@ -269,7 +269,8 @@ __device__ __forceinline__ void join_out(const PagedArgs& a, int item, int hl, i
   const float inv = j.M == -INFINITY ? 0.f : 1.f / (j.L + __expf(sk - j.M));
   if (a.weights && lane == 0 && d0 == 0) {
     const float top = fmaxf(j.M, sk);
-    a.lse2[(int64_t)item * a.hn + hl] = (top + logf(j.L * expf(j.M - top) + expf(sk - top))) * kLog2e;
+    a.lse2[(int64_t)item * a.hn + hl] =
+        j.M == -INFINITY ? INFINITY : (top + logf(j.L * expf(j.M - top) + expf(sk - top))) * kLog2e;
   }
 #pragma unroll
   for (int i = 0; i < 8; ++i) x[i] = j.x[i] * inv;

@@ -57,7 +57,7 @@ struct PagedArgs {
   int hn, hgroups, kt, G;
   int4* cut;         // [G] the item that begins in the block and is cut: item or -1, its last block, its slot
   float* part;       // [2 G][2 hn + hn D] segments: max (natural log), sum, accumulator
-  float* lse2;       // [items][hn] log2 of the softmax denominator (weights only)
+  float* lse2;       // [items][hn] log2 of the softmax denominator, +inf if no key counts (weights only)
   int item_tiles;    // at most that many tiles an item
   float* tile_ref;   // [items][item_tiles][hn] reference of each tile's probabilities, log2 (weights only)
   uint16_t* tile_p;  // [items][item_tiles][kt][hn] probabilities against it, bf16 (weights only); of the

@@ -498,7 +498,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
         if (sg.whole) {
           const float den = l + exp2f(sink_t[st] - m);
           inv_s[st] = none ? 0.f : 1.f / den;
-          if (a.weights) a.lse2[(int64_t)sg.item * kH + st] = none ? sink_t[st] : m + log2f(den);
+          if (a.weights) a.lse2[(int64_t)sg.item * kH + st] = none ? INFINITY : m + log2f(den);
         } else {
           part[st] = none ? -INFINITY : m * 0.6931471805599453f;  // natural-log units
           part[kH + st] = l;

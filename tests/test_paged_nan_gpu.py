@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import long_context_hybrid_kv_b200 as L
-from gpu_util import check_ok
+from gpu_util import check_ok, f32
 from test_paged_gpu import Case
 
 pytestmark = pytest.mark.gpu
@@ -113,3 +113,21 @@ def test_nan_in_a_sink(kind, spread):
     assert same(first[0][:, keep], then[0][:, keep])
     for b, n in enumerate(c.lens):
         assert torch.isnan(then[1][b, :n]).all() and same(first[1][b, n:], then[1][b, n:])
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("lens", [[40], [3000]])
+def test_sinks_of_minus_infinity(kind, lens):
+    """No sink at all; then no key either (every page is bad): zeros, no NaN."""
+    c = Case(f"mi{kind}", lens, 64, m=16, spare=0, **{**KINDS[kind], "W": 0})
+    c.sink[:] = -np.inf
+    c.d_sink.copy_(f32(c.sink))
+    w = torch.full((c.B, max(lens) + 1), 7.0, dtype=torch.bfloat16, device="cuda")
+    c.run(weights=w)
+    check_ok()
+    c.check(weights=w)
+    c.d_table.fill_(-1)
+    c.run(weights=w)
+    rc, bits = L.ds4a_check()
+    assert rc == L.DS4A_EDEVICE and bits == 1
+    assert (c.out == 0).all() and (w[:, :lens[0]] == 0).all() and (w[:, lens[0]:] == 7.0).all()
