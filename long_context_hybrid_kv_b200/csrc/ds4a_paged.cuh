@@ -127,6 +127,14 @@ constexpr int kPagedWhole = 4, kPagedLeast = 2;
 constexpr int kPagedCost = 6;  // of a segment besides its tiles, in tiles (a second segment takes 7 to 8 us, four tiles; 4 to 6 measure alike)
 constexpr int kPagedJoin = 4;  // of the joining, in tiles
 
+// Where piece j of an item of n tiles in p equal pieces begins: floor(j n / p)
+// for j <= p, by quotient and remainder, since 296 pieces of 2^25 tiles pass 32
+// bits (j rem < p^2 does not).
+__host__ __device__ constexpr int paged_piece(int j, int n, int p) {
+  const unsigned q = (unsigned)n / (unsigned)p, rem = (unsigned)n - q * (unsigned)p;
+  return (int)((unsigned)j * q + (unsigned)j * rem / (unsigned)p);
+}
+
 // More items than blocks: the blocks that take part, where block c's range
 // begins before its ends are moved, and the block that holds tile t.
 __device__ __forceinline__ int paged_blocks(int total, int G) { return min(G, (total + 1) / 2); }
@@ -259,8 +267,8 @@ __device__ __forceinline__ PagedRange paged_range(const PagedArgs& a, int c, int
             const int at = c - blocks - __shfl_sync(0xffffffffu, pi - p, l), g = at / p_l, j = at - g * p_l;
             r.kind = 0;
             r.item = (b0 + l) * hg + g;
-            r.t0 = (int)((unsigned)(j * n_l) / (unsigned)p_l);
-            r.t1 = (int)((unsigned)((j + 1) * n_l) / (unsigned)p_l);
+            r.t0 = paged_piece(j, n_l, p_l);
+            r.t1 = paged_piece(j + 1, n_l, p_l);
             r.last = c - j + p_l - 1;
             break;
           }
