@@ -526,8 +526,10 @@ size_t ds4a_paged_evict_workspace(const ds4a_paged_kv* kv, int B);
 /*
  * ds4a_paged_evict -- bound a paged cache to `budget` entries a sequence, by
  * accumulated attention weight (for layers that attend to every entry; no
- * counterpart on the pages of the sources).  For each sequence, with its n
- * slots in use (as above; at most n_slots of them):
+ * counterpart on the pages of the sources).  For each sequence, with its n =
+ * max(0, floor((p + 1) / m) - drop[b]) slots in use (if there are more than
+ * n_slots, entries that found no slot among them, DS4A_DEV_BAD_INDEX is
+ * recorded and the sequence left as it is):
  *   1. acc[s] += weights[s] for s < n (weights NULL: nothing is added);
  *   2. if n > budget: of its n entries the `recent` youngest stay, and of the
  *      others those of the largest acc (ties: the lower slot; NaN counts as

@@ -38,6 +38,20 @@ __device__ __forceinline__ unsigned int evict_key(float acc, bool protect) {
   return u == 0x80000000u ? f2key(0.f) : f2key(acc);
 }
 
+// A sequence that is left as it is: at a negative position, or with more
+// entries than slots (those behind cannot be told apart from free ones, and a
+// cut of the others would hand out their numbers); recorded.  The same in all
+// blocks of a cluster.
+__device__ __forceinline__ bool evict_refuses(const EvictArgs& a, int b, int pos, int closed, int gone) {
+  const bool bad_pos = pos < 0;
+  if (!bad_pos && (int64_t)closed - gone <= a.cap) return false;
+  if (threadIdx.x == 0) {
+    raise_err(a.err, bad_pos ? DS4A_DEV_BAD_POS : DS4A_DEV_BAD_INDEX);
+    a.moves[b] = 0;
+  }
+  return true;
+}
+
 // exclusive prefix of two 16-bit-safe counts over the block, and their totals
 __device__ __forceinline__ int2 block_scan(int x, int y, int2* sums, int2* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -74,17 +88,10 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictArgs 
   const int b = blockIdx.x, tid = threadIdx.x;
   pdl_trigger();
   pdl_wait();
-  const int pos = a.q_pos[b];
-  if (pos < 0) {
-    if (tid == 0) {
-      raise_err(a.err, DS4A_DEV_BAD_POS);
-      a.moves[b] = 0;
-    }
-    return;
-  }
-  const int gone = a.drop[b];
-  const int closed = (int)(((int64_t)pos + 1) / a.m);
-  const int n = max(0, min(closed - gone, a.cap));
+  const int pos = a.q_pos[b], gone = a.drop[b];
+  const int closed = (int)(((unsigned)pos + 1u) / (unsigned)a.m);
+  if (evict_refuses(a, b, pos, closed, gone)) return;
+  const int n = max(0, closed - gone);
   float* acc = a.acc + (int64_t)b * a.stride;
   int32_t* entry = a.entry + (int64_t)b * a.stride;
   const uint16_t* w = a.w ? a.w + (int64_t)b * a.w_stride : nullptr;
@@ -175,7 +182,7 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictArgs 
     entry[to] = e < 0 ? from + gone : e;
   }
   __syncthreads();
-  // slots behind the kept ones start over (n may stop short of stale ones of a longer cache)
+  // slots behind the kept ones start over
   for (int s = a.budget + tid; s < a.cap; s += kThreads) {
     acc[s] = 0.f;
     entry[s] = -1;
@@ -247,15 +254,9 @@ __global__ void __launch_bounds__(kThreads, 1) evict_keep_kernel(const EvictArgs
   pdl_trigger();
   pdl_wait();
   const int pos = a.q_pos[b], gone = a.drop[b];
-  if (pos < 0) {
-    if (tid == 0) {
-      raise_err(a.err, DS4A_DEV_BAD_POS);
-      a.moves[b] = 0;
-    }
-    return;
-  }
   const int closed = (int)(((unsigned)pos + 1u) / (unsigned)a.m);
-  const int n = max(0, min(closed - gone, a.cap)), budget = a.budget;
+  if (evict_refuses(a, b, pos, closed, gone)) return;
+  const int n = max(0, closed - gone), budget = a.budget;
   float* acc = a.acc + (int64_t)b * a.stride;
   int32_t* entry = a.entry + (int64_t)b * a.stride;
   const uint16_t* w = a.w ? a.w + (int64_t)b * a.w_stride : nullptr;
