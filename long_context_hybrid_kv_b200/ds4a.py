@@ -147,8 +147,11 @@ def _ptr(t):
 def _stream(stream):
     if stream is None:
         import torch
-        # torch.cuda.current_stream().cuda_stream without its Stream object (3 us a call)
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        # torch.cuda.current_stream().cuda_stream without its Stream object (3 us a call), where torch offers it
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        if raw is None:
+            return torch.cuda.current_stream().cuda_stream
+        return raw(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream

@@ -202,3 +202,19 @@ def test_binding_fails_loudly_without_library(monkeypatch, tmp_path):
     monkeypatch.setattr(mod, "LIB_PATH", str(tmp_path / "missing.so"))
     with pytest.raises(RuntimeError, match="missing"):
         mod.lib()
+
+
+@pytest.mark.parametrize("offered", [True, False])
+def test_current_stream_with_and_without_torchs_short_way(monkeypatch, offered):
+    import types
+
+    import torch
+    from long_context_hybrid_kv_b200 import ds4a
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 3)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda: types.SimpleNamespace(cuda_stream=71))
+    if offered:
+        monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: 70 + dev, raising=False)
+    else:
+        monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream", raising=False)
+    assert ds4a._stream(None) == (73 if offered else 71)
+    assert ds4a._stream(5) == 5 and ds4a._stream(types.SimpleNamespace(cuda_stream=9)) == 9
