@@ -159,7 +159,6 @@ int ds4a_compress(const ds4a_layer_cfg* cfg, int B, int T_tok, int tok_begin, in
   a.bias_a = bias_a; a.bias_b = bias_b; a.norm_g = norm_g;
   a.entry_begin = entry_begin; a.entry_end = entry_end;
   a.pool = pool; a.pool_bstride = pool_bstride;
-  a.pg_size = 0;
   a.app_pos = nullptr; a.ring = nullptr; a.ring_cap = 0; a.n_cap = 0;
   a.qfmt = 0; a.qpool = nullptr; a.q_bstride = 0; a.q_row = 0; a.qscales = nullptr; a.qs_bstride = 0;
   fill_rope_theta(&a.rope, a.rope_dim, cfg->rope_base);
@@ -220,7 +219,6 @@ static int build_append_args(const ds4a_layer_cfg* cfg, int B, int c, const int3
   a.bias_a = bias_a; a.bias_b = bias_b; a.norm_g = norm_g;
   a.entry_begin = 0; a.entry_end = 1;
   a.pool = pool; a.pool_bstride = pool_bstride;
-  a.pg_size = 0;
   a.app_pos = pos; a.ring = state; a.ring_cap = overlap ? 2 * m : m; a.n_cap = N_cap;
   a.qfmt = qfmt; a.qpool = qpool; a.qscales = qscales;
   a.q_row = qfmt == 1 ? kv_fp8_row_bytes(c, R) : c / 2;
@@ -651,7 +649,7 @@ int ds4a_paged_append(const ds4a_layer_cfg* cfg, const ds4a_paged_kv* kv, int B,
   if (kv->format == DS4A_MX_KV_FP8 && !norm_g && cfg->rope_dim != 0) return DS4A_EUNSUPPORTED;
   const int fmt = kv->format == DS4A_MX_KV_FP8 ? 1 : 0;
   // every entry number may come: the slot is checked on the device
-  CompressArgs a;
+  PagedCompressArgs a;
   static ds4a_bf16* const kSomePool = reinterpret_cast<ds4a_bf16*>(16);  // never followed: the pages are
   const int rc = build_append_args(cfg, B, c, pos, ca, cb, za, zb, bias_a, bias_b, norm_g, state, INT32_MAX,
                                    fmt ? nullptr : kSomePool, INT64_MAX - 1, fmt,

@@ -76,7 +76,7 @@ __device__ __forceinline__ const uint16_t* term_row(const CompressArgs& a, bool 
 
 // Paged output: the row of entry i of sequence b among all pages' rows, or -1
 // (a slot outside the table or a bad page).
-__device__ __forceinline__ int64_t page_row(const CompressArgs& a, int b, int i) {
+__device__ __forceinline__ int64_t page_row(const PagedCompressArgs& a, int b, int i) {
   const int slot = i - (a.pg_drop ? a.pg_drop[b] : 0);
   if (slot < 0 || slot >= a.pg_cap) return -1;
   const int pg = slot / a.pg_size, ph = a.pg_table[(int64_t)b * a.pg_stride + pg];
@@ -88,7 +88,8 @@ __device__ __forceinline__ int64_t page_row(const CompressArgs& a, int b, int i)
 // or -1 (no entry closes, a bad position, or an entry past the pool).
 // *row: the entry's row among the pages (paged output only; looked up here
 // once, so that what was checked is what is written).
-__device__ __forceinline__ int closing_entry(const CompressArgs& a, int b, int p, bool report, int64_t* row) {
+template <class Args>
+__device__ __forceinline__ int closing_entry(const Args& a, int b, int p, bool report, int64_t* row) {
   if (p < 0) {
     if (report) raise_err(a.err, DS4A_DEV_BAD_POS);
     return -1;
@@ -99,7 +100,7 @@ __device__ __forceinline__ int closing_entry(const CompressArgs& a, int b, int p
     if (report) raise_err(a.err, DS4A_DEV_BAD_INDEX);
     return -1;
   }
-  if (a.pg_size != 0) {
+  if constexpr (Args::kPaged) {
     *row = page_row(a, b, i);
     if (*row < 0) {
       if (report) raise_err(a.err, DS4A_DEV_BAD_INDEX);
@@ -111,12 +112,13 @@ __device__ __forceinline__ int closing_entry(const CompressArgs& a, int b, int p
 
 // First element of entry i of sequence b in the bf16 pool, and its byte row
 // in a block-scaled one (row: as closing_entry gave it).
-__device__ __forceinline__ uint16_t* entry_dst(const CompressArgs& a, int b, int i, int64_t row) {
-  return a.pool + (a.pg_size != 0 ? row * a.c : (int64_t)b * a.pool_bstride + (int64_t)i * a.c);
+template <class Args>
+__device__ __forceinline__ uint16_t* entry_dst(const Args& a, int b, int i, int64_t row) {
+  return a.pool + (Args::kPaged ? row * a.c : (int64_t)b * a.pool_bstride + (int64_t)i * a.c);
 }
-__device__ __forceinline__ uint8_t* entry_dst_mx(const CompressArgs& a, int b, int i, int64_t row) {
-  return a.qpool +
-         (a.pg_size != 0 ? row * a.q_row : (int64_t)b * a.q_bstride + (int64_t)i * a.q_row);
+template <class Args>
+__device__ __forceinline__ uint8_t* entry_dst_mx(const Args& a, int b, int i, int64_t row) {
+  return a.qpool + (Args::kPaged ? row * a.q_row : (int64_t)b * a.q_bstride + (int64_t)i * a.q_row);
 }
 
 // Append mode: store the new token's rows of every stream (position p >= 0)
@@ -149,7 +151,8 @@ __device__ __forceinline__ void append_token(const CompressArgs& a, int b, int p
 // the block-scaled case every lane of the warp calls it, the warp holding 64
 // consecutive channels that start at a multiple of 64 (two 32-channel
 // blocks, one per half-warp).
-__device__ __forceinline__ void store_entry_pair(const CompressArgs& a, int b, int i, int64_t prow, int ch, float x0,
+template <class Args>
+__device__ __forceinline__ void store_entry_pair(const Args& a, int b, int i, int64_t prow, int ch, float x0,
                                                  float x1, uint16_t* dst) {
   const unsigned int packed = f2_to_bf2x2(x0, x1);
   if (a.qfmt == 0) {
@@ -286,8 +289,8 @@ __global__ void __launch_bounds__(kShortThreads) compress_short_kernel(const __g
   compress_short(a);
 }
 
-template <int V>
-__device__ __forceinline__ void compress_body(const CompressArgs& a) {
+template <int V, class Args>
+__device__ __forceinline__ void compress_body(const Args& a) {
   extern __shared__ float csm[];
   const int c = a.c, m = a.m;
   const int NC = c / V;
@@ -427,8 +430,8 @@ __device__ __forceinline__ void compress_body(const CompressArgs& a) {
   }
 }
 
-template <int V>
-__global__ void __launch_bounds__(kCompressThreads) compress_kernel(const __grid_constant__ CompressArgs a) {
+template <int V, class Args>
+__global__ void __launch_bounds__(kCompressThreads) compress_kernel(const __grid_constant__ Args a) {
   compress_body<V>(a);
 }
 
@@ -457,8 +460,8 @@ static bool short_entry(const CompressArgs& a) {
 // blocks add their RMSNorm sums of squares the same way, and each writes
 // its channels.  Same arithmetic as compress_kernel (log2-unit softmax with a
 // lazy reference), merged in a different order.
-template <int V>
-__global__ void __launch_bounds__(kCompressThreads) compress_split_kernel(CompressArgs a, int Z) {
+template <int V, class Args>
+__global__ void __launch_bounds__(kCompressThreads) compress_split_kernel(Args a, int Z) {
   extern __shared__ float csm[];
   namespace cg = cooperative_groups;
   cg::cluster_group cl = cg::this_cluster();
@@ -656,8 +659,9 @@ __device__ __forceinline__ void merge_partial(float& mx, float& l, float& acc, f
   mx = M;
 }
 
+template <class Args>
 __global__ void __cluster_dims__(kChanZ, 1, 1) __launch_bounds__(kChanThreads, 2)
-    compress_chan_kernel(const __grid_constant__ CompressArgs a) {
+    compress_chan_kernel(const __grid_constant__ Args a) {
   constexpr int V = 8, NC = kChanNC, G = kChanThreads / NC;
   namespace cg = cooperative_groups;
   cg::cluster_group cl = cg::this_cluster();
@@ -826,7 +830,8 @@ cudaError_t launch_compress_jobs(const CompressArgs* jobs, int n_jobs, cudaStrea
   return cudaSuccess;
 }
 
-cudaError_t launch_compress(const CompressArgs& a, cudaStream_t s) {
+template <class Args>
+static cudaError_t launch_compress_of(const Args& a, cudaStream_t s) {
   // append mode: one (possible) entry per sequence
   const int n = a.app_pos != nullptr ? 1 : a.entry_end - a.entry_begin;
   if (n <= 0 || a.B <= 0) return cudaSuccess;
@@ -834,15 +839,17 @@ cudaError_t launch_compress(const CompressArgs& a, cudaStream_t s) {
   const int NC = a.c / V;
   const int G = NC >= kCompressThreads ? 1 : kCompressThreads / NC;
   const int n_terms = a.cb != nullptr ? 2 * a.m : a.m;
-  if (short_entry(a)) {
-    TraceScope tr("compress", s);
-    return launch_pdl(compress_short_kernel, dim3(n, a.B), dim3(kShortThreads), 0, s, a);
+  if constexpr (!Args::kPaged) {
+    if (short_entry(a)) {  // (never in append mode, which pages imply)
+      TraceScope tr("compress", s);
+      return launch_pdl(compress_short_kernel, dim3(n, a.B), dim3(kShortThreads), 0, s, a);
+    }
   }
   // long entries of 512 channels, few of them (decode): an 8-block cluster
   // per entry, 64 channels per block
   if (V == 8 && a.c == kChanC && n_terms >= 64 && (int64_t)n * a.B <= 32) {
     TraceScope tr("compress", s);
-    return launch_pdl(compress_chan_kernel, dim3(n * kChanZ, a.B), dim3(kChanThreads), 0, s, a);
+    return launch_pdl(compress_chan_kernel<Args>, dim3(n * kChanZ, a.B), dim3(kChanThreads), 0, s, a);
   }
   // other long entries, few of them: split each entry's terms over a cluster
   int Z = 1;
@@ -851,21 +858,24 @@ cudaError_t launch_compress(const CompressArgs& a, cudaStream_t s) {
   if (Z > 1) {
     const size_t smem = (size_t)(3 * G * a.c + 3 * a.c + a.c / Z) * sizeof(float);
     static std::atomic<int> cache_s[kMaxDevices];
-    cudaError_t e = ensure_smem(compress_split_kernel<8>, (int)smem, cache_s);
+    cudaError_t e = ensure_smem(compress_split_kernel<8, Args>, (int)smem, cache_s);
     if (e != cudaSuccess) return e;
     TraceScope tr("compress", s);
-    return launch_pdl_cluster(compress_split_kernel<8>, dim3(n * Z, a.B), dim3(kCompressThreads), smem, s, Z, a,
+    return launch_pdl_cluster(compress_split_kernel<8, Args>, dim3(n * Z, a.B), dim3(kCompressThreads), smem, s, Z, a,
                               Z);
   }
   const size_t smem = (size_t)(3 * G * a.c + a.c) * sizeof(float);
   static std::atomic<int> cache8[kMaxDevices], cache2[kMaxDevices];
-  cudaError_t e = V == 8 ? ensure_smem(compress_kernel<8>, (int)smem, cache8)
-                         : ensure_smem(compress_kernel<2>, (int)smem, cache2);
+  cudaError_t e = V == 8 ? ensure_smem(compress_kernel<8, Args>, (int)smem, cache8)
+                         : ensure_smem(compress_kernel<2, Args>, (int)smem, cache2);
   if (e != cudaSuccess) return e;
   TraceScope tr("compress", s);
-  return V == 8 ? launch_pdl(compress_kernel<8>, dim3(n, a.B), dim3(kCompressThreads), smem, s, a)
-                : launch_pdl(compress_kernel<2>, dim3(n, a.B), dim3(kCompressThreads), smem, s, a);
+  return V == 8 ? launch_pdl(compress_kernel<8, Args>, dim3(n, a.B), dim3(kCompressThreads), smem, s, a)
+                : launch_pdl(compress_kernel<2, Args>, dim3(n, a.B), dim3(kCompressThreads), smem, s, a);
 }
+
+cudaError_t launch_compress(const CompressArgs& a, cudaStream_t s) { return launch_compress_of(a, s); }
+cudaError_t launch_compress(const PagedCompressArgs& a, cudaStream_t s) { return launch_compress_of(a, s); }
 
 // ===========================================================================
 // Indexer score, CUDA-core form (any H_I, D_I <= 128)
