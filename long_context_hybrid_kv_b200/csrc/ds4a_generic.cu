@@ -94,8 +94,9 @@ __device__ __forceinline__ int closing_entry(const Args& a, int b, int p, bool r
     if (report) raise_err(a.err, DS4A_DEV_BAD_POS);
     return -1;
   }
-  if ((p + 1) % a.m != 0) return -1;
-  const int i = (p + 1) / a.m - 1;
+  const unsigned int n = (unsigned int)p + 1u;  // (the last position's passes 31 bits)
+  if (n % (unsigned int)a.m != 0) return -1;
+  const int i = (int)(n / (unsigned int)a.m - 1u);
   if (i >= a.n_cap) {
     if (report) raise_err(a.err, DS4A_DEV_BAD_INDEX);
     return -1;
