@@ -33,7 +33,11 @@
  *   therefore not be written by a still-running library kernel: produce
  *   them with ordinary stream work (any kernel or copy that is not part of
  *   this library orders fully), never by feeding one call's output buffer
- *   to the next call as an input.
+ *   to the next call as an input.  What a call documents as written by
+ *   another one may come straight from it: pools, pages, states, indices,
+ *   drop, the attention's output in a projection, its weights in an eviction,
+ *   and quantised matrices (the quantisers order fully).  A page table is an
+ *   input: no call writes one.
  * - Storage types: ds4a_bf16 is a bfloat16 bit pattern.  Arithmetic is
  *   float32 (bf16 x bf16 products accumulated in float32 on tensor cores).
  * - Layouts: contiguous row-major, dimensions listed outermost first; batch
@@ -475,7 +479,12 @@ size_t ds4a_paged_attend_workspace(const ds4a_layer_cfg* cfg, const ds4a_paged_k
 /*
  * ds4a_paged_attend -- ds4a_sparse_attend / ds4a_hca_attend of one new token
  * per sequence over a paged cache: the same keys, softmax with sink, and
- * rotations, the keys split over the GPU and joined.
+ * rotations, the keys split over the GPU and joined.  On the tensor cores
+ * (rows of 512) the prepared query and the probabilities are rounded to bf16
+ * before their products, as in the contiguous calls; logits, softmax sums and
+ * outputs are float32 until they are stored.  A NaN or an infinity in a
+ * query, a sink or a row in use shows in every output and weight that it
+ * reaches, and in no other.  (A sink of minus infinity is no sink.)
  *
  *   q_pos   device int32 [B].  A negative position is recorded as
  *           DS4A_DEV_BAD_POS and its output and weights are left as they were
@@ -550,7 +559,9 @@ size_t ds4a_paged_evict_workspace(const ds4a_paged_kv* kv, int B);
  *   budget  1 .. n_slots; recent 0 .. budget
  *   ws      device workspace of ds4a_paged_evict_workspace(...) bytes
  * Sequences must not share pages.  The pages behind the budget may be handed
- * out again once the call is done.
+ * out again once the call is done.  A row that would move from or to a bad
+ * page stays where it is (DS4A_DEV_BAD_INDEX), its acc and number move: bad
+ * pages of slots in use make the cache unsound.
  */
 int ds4a_paged_evict(const ds4a_layer_cfg* cfg, const ds4a_paged_kv* kv, int B, const int32_t* q_pos,
                      const ds4a_bf16* weights, int64_t w_stride, int budget, int recent, int n_slots, float* acc,

@@ -18,8 +18,11 @@
 // their exponents, has; it ends as soon as a bound leaves exactly `budget`),
 // then two scans rank holes and movers.  Bound by that chain of barriers: 9.4
 // us for 32 sequences of 1024 slots, 24 for 8 of 7596, 66 for 32 of 32768.
-// evict_select_kernel does the same by radix select from memory, for more
-// slots.  evict_move_kernel, over the whole GPU: the rows, bound by
+// evict_select_kernel does the same by radix select from memory, one block a
+// sequence, where that leaves a thread more than 32 slots: above 262144 slots,
+// and from 32769 slots on in batches that leave no SM for larger clusters (37
+// sequences have four blocks each up to 131072 slots, 74 two up to 65536, 75
+// one up to 32768).  evict_move_kernel, over the whole GPU: the rows, bound by
 // memory; few are moved by the first kernel itself.
 #include "ds4a_evict.cuh"
 

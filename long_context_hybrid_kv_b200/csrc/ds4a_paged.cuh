@@ -60,8 +60,9 @@ struct PagedArgs {
   float* lse2;       // [items][hn] log2 of the softmax denominator, +inf if no key counts (weights only)
   int item_tiles;    // at most that many tiles an item
   float* tile_ref;   // [items][item_tiles][hn] reference of each tile's probabilities, log2 (weights only)
-  uint16_t* tile_p;  // [items][item_tiles][kt][hn] probabilities against it, bf16 (weights only); of the
-                     // tensor-core kernel the 16-byte piece c of a key's row at c ^ (key % 8)
+  uint16_t* tile_p;  // [items][item_tiles][kt][hn] probabilities against it (weights only), bf16: half the
+                     // bytes, and their sum over the heads, which averages the roundings, goes out as bf16;
+                     // of the tensor-core kernel the 16-byte piece c of a key's row at c ^ (key % 8)
   unsigned int* err;
   RopeTheta rope;
 };

@@ -17,10 +17,11 @@
 // the codes).  (A ring of 48-key tiles, or MMAs of two warps in turn, were
 // slower; integer expansion of the codes 114 us instead of 89.)
 //
-// q^ and P are rounded to bf16, which the MMA takes (half a step, 2^-9, each,
-// which the softmax and the sum over keys average: 0.0026 of the output's
-// largest value against the 0.0017 of the output's own rounding); logits,
-// maxima, sums and O stay in float32.
+// q^ and P are rounded to bf16, which the MMA takes with bf16 rows (at most
+// half a step, 2^-8, each, which the softmax and the sum over keys average: an
+// output is off by 0.0024 to 0.0027, root mean square, against the 0.0017 of
+// its own rounding; the low halves would take 64 KiB of the ring, and as many
+// MMAs again of the second product); logits, maxima, sums and O stay in float32.
 //
 // Thread block (one per SM, 640 threads):
 //   warps 0-7    q^ of every segment, softmax, epilogue: two warps per TMEM
@@ -40,8 +41,8 @@
 // Of a small call the prologue is half: code that runs once waits for its
 // instructions, so it is short and not unrolled (b1 x 64 entries 13.9 -> 11.4
 // us).  In a graph of calls with the window of 128: b1 x 8192 entries 21 us,
-// b32 x 1024 32 us, b32 x 8192 86 us (272 MB of rows: 3.2 TB/s), b256 x 512
-// selected 68 us.
+// b32 x 1024 32 us, b32 x 8192 86 to 109 us from GPU to GPU (272 MB of rows: 2.5
+// to 3.2 TB/s), b256 x 512 selected 68 us.
 #include "ds4a_paged.cuh"
 #include "ds4a_tc.cuh"
 

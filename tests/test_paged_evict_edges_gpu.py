@@ -1,4 +1,5 @@
-"""Eviction at its edges: more entries in use than the call has slots for."""
+"""Eviction at its edges: more entries in use than the call has slots for,
+large batches of large caches."""
 import numpy as np
 import pytest
 import torch
@@ -7,7 +8,7 @@ import long_context_hybrid_kv_b200 as L
 import paged_ref as P
 from gpu_util import bf, bits, f32, i32
 from oracle import ds4a_oracle as O
-from test_paged_schedule_gpu import bf_bits
+from test_paged_schedule_gpu import bf_bits, evict_many
 
 pytestmark = pytest.mark.gpu
 
@@ -65,3 +66,8 @@ def test_more_entries_than_slots_is_recorded(B, n_slots, budget, weights):
         follow(b, wide)
     agree()
     assert drop[1] == 5 + n_slots + 1 - budget
+
+
+def test_batch_that_leaves_no_room_for_clusters():
+    # more slots than one block holds: the form that selects from memory
+    evict_many("no clusters", 75, 33000, 16000, 7, D=8)
