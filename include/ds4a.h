@@ -79,7 +79,7 @@ enum {
 
 /* Bits of the device error word (ds4a_check). */
 enum {
-  DS4A_DEV_BAD_INDEX = 1u, /* an index >= N_c or < -1 was skipped             */
+  DS4A_DEV_BAD_INDEX = 1u, /* an index, slot or page out of range was skipped */
   DS4A_DEV_BAD_POS = 2u,   /* a negative query position was skipped          */
   DS4A_DEV_TIMEOUT = 4u    /* a bounded wait inside a kernel ran out          */
 };

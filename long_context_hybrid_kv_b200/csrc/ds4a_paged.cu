@@ -429,6 +429,9 @@ __global__ void __launch_bounds__(kJoinThreads) paged_weights_kernel(const __gri
   }
 }
 
+// bits of the heads h, h + 1 in a word that lie below nh
+__device__ __forceinline__ unsigned int head_pair(int h, int nh) { return (h < nh ? 0xFFFFu : 0u) | (h + 1 < nh ? 0xFFFF0000u : 0u); }
+
 // The same for the tensor-core kernel's tiles (64 keys x 64 heads, swizzled),
 // a warp a tile and no block barrier: a load covers four keys' rows, lane l
 // the piece l % 8 of key l / 8, so that a lane's heads alternate between two
@@ -452,6 +455,18 @@ __global__ void __launch_bounds__(kJoinThreads) paged_weights64_kernel(const __g
       uint4 v[16];
 #pragma unroll
       for (int i = 0; i < 16; ++i) v[i] = p[32 * i];
+      if ((g + 1) * 64 > a.H) {
+        // heads that the group does not have: their query is 0, and 0 times an infinite row is NaN
+        const int nh = a.H - g * 64;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int h0 = 8 * (piece ^ (row + 4 * (i & 1)));
+          v[i].x &= head_pair(h0, nh);
+          v[i].y &= head_pair(h0 + 2, nh);
+          v[i].z &= head_pair(h0 + 4, nh);
+          v[i].w &= head_pair(h0 + 6, nh);
+        }
+      }
       __syncwarp();
 #pragma unroll
       for (int i = 0; i < 2; ++i) {

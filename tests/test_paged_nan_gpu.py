@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import long_context_hybrid_kv_b200 as L
-from gpu_util import check_ok, f32
+from gpu_util import bf, check_ok, f32
 from test_paged_gpu import Case
 
 pytestmark = pytest.mark.gpu
@@ -131,3 +131,35 @@ def test_sinks_of_minus_infinity(kind, lens):
     rc, bits = L.ds4a_check()
     assert rc == L.DS4A_EDEVICE and bits == 1
     assert (c.out == 0).all() and (w[:, :lens[0]] == 0).all() and (w[:, lens[0]:] == 7.0).all()
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("spread", ["whole", "pieces", "ranges"])
+@pytest.mark.parametrize("which", ["one", "front"])
+@pytest.mark.filterwarnings("ignore:invalid value")
+def test_infinity_in_rows_in_use(kind, spread, which):
+    """Logits of plus and of minus infinity: NaN where the plain form has it (the
+    weights are those of the heads that are there)."""
+    lens = SPREADS[spread]
+    b = len(lens) // 2 - 1
+
+    def change(c):
+        n, d = c.lens[b], c.D - c.R + 4  # (a dim that FP8 rows hold in bf16)
+        s = dict(one=np.array([n // 3]), front=np.arange(n // 2))[which]
+        at = c.table[b][s // 64], s % 64
+        if c.fp8:
+            c.pages_np[at[0], at[1], c.D - c.R + 8] = INF & 255
+            c.pages_np[at[0], at[1], c.D - c.R + 9] = INF >> 8
+            c.pages.copy_(torch.from_numpy(c.pages_np))
+        else:
+            c.pages_np[at[0], at[1], d] = INF
+            c.pages.copy_(bf(c.pages_np))
+
+    c, first, then = twice(f"ir{kind}{spread}{which}", lens, change, **KINDS[kind])
+    out, w, _, _ = c.ref(b)
+    nan = np.isnan(out)
+    assert nan.any()
+    assert np.array_equal(torch.isnan(then[0][b]).cpu().numpy(), nan)
+    assert np.array_equal(torch.isnan(then[1][b, :lens[b]]).cpu().numpy(), np.isnan(w))
+    keep = [i for i in range(c.B) if i != b]
+    assert same(first[0][keep], then[0][keep]) and same(first[1][keep], then[1][keep])
