@@ -250,8 +250,8 @@ __device__ __forceinline__ void join_sum(const PagedArgs& a, int c0, int slot0, 
     if (s > s0) load(s);
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
-      if (m[i] == -INFINITY) continue;  // (a segment without a key that counts may hold anything)
-      const float e = __expf(m[i] - j.M);
+      // (a segment without a key that counts holds zeros, or NaN where an infinite row gave a logit of -inf)
+      const float e = m[i] == -INFINITY ? 0.f : __expf(m[i] - j.M);
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         j.x[4 * k] = fmaf(v[i][k].x, e, j.x[4 * k]);

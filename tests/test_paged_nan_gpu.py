@@ -163,3 +163,28 @@ def test_infinity_in_rows_in_use(kind, spread, which):
     assert np.array_equal(torch.isnan(then[1][b, :lens[b]]).cpu().numpy(), np.isnan(w))
     keep = [i for i in range(c.B) if i != b]
     assert same(first[0][keep], then[0][keep]) and same(first[1][keep], then[1][keep])
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.filterwarnings("ignore:invalid value")
+def test_infinity_in_all_rows_of_a_piece(kind):
+    """The first piece of a cut sequence, one tile: logits of minus infinity
+    give it no weight, but 0 times infinity is NaN."""
+    c = Case(f"ip{kind}", [5000], 64, m=16, spare=0, **KINDS[kind])
+    s, d = np.arange(32 if kind == "generic" else 64), c.D - c.R + 4
+    at = c.table[0][s // 64], s % 64
+    if c.fp8:
+        c.pages_np[at[0], at[1], c.D - c.R + 8] = INF & 255
+        c.pages_np[at[0], at[1], c.D - c.R + 9] = INF >> 8
+        c.pages.copy_(torch.from_numpy(c.pages_np))
+    else:
+        c.pages_np[at[0], at[1], d] = INF
+        c.pages.copy_(bf(c.pages_np))
+    c.q[0, 1] = c.q[0, 0] ^ 0x8000  # heads of either sign
+    c.d_q.copy_(bf(c.q))
+    c.run()
+    check_ok()
+    out, _, _, _ = c.ref(0)
+    nan = np.isnan(out)
+    assert nan.any() and not nan.all()
+    assert np.array_equal(torch.isnan(c.out[0]).cpu().numpy(), nan)
